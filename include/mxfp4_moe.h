@@ -263,6 +263,26 @@ int moe_mxfp4_calibrate(const uint16_t* x, const uint16_t* router_w, const uint1
                         const uint8_t* d_blocks, const uint8_t* d_scales, const float* d_bias,
                         int E, int k, int T, int H, int I, float* act_scale_out, void* stream);
 
+/* rmsnorm_residual -- the norm around the attention projections and the expert layer, with
+ * the residual's addition and the A-FP8 cast of what follows ("gpt-oss-120b-mxfp4-fp8attn-v2",
+ * Model Details: FP8 E4M3 inputs of Q/K/V/O). Per row t:
+ *   h = bf16(x + residual)  (written to sum_out; h = x when residual is NULL)
+ *   n = h * weight / sqrt(mean(h^2) + eps)                        (fp32)
+ *   y = bf16(n);  q = e4m3(n / s), saturating at +-448, round to nearest even
+ * with s = *act_scale (static; a HOST pointer to one float) or, with q_scale, one scale per
+ * token s_t = max|n_t| / 448 written to q_scale (1 for a row of zeros; fp8_linear_fused takes
+ * both). x, residual: device bf16 rows ldx / ldr elements apart (multiples of 8, >= H);
+ * weight: device bf16 (H); sum_out, y: device bf16 (T, H); q: device uint8 (T, H) E4M3 codes;
+ * q_scale: device fp32 (T). residual and sum_out go together; y, q or both are asked for; q
+ * comes with exactly one of act_scale and q_scale. sum_out may be the residual's or x's own
+ * memory, and y may be x's, where that input is dense (ld = H); any other overlap is the
+ * caller's error. Limits: H % 8 == 0 (MXMOE_EALIGN), H <= 32768 (MXMOE_EUNSUPPORTED), eps in
+ * [1e-12, 1], act_scale in [1e-30, 1e30], every pointer 16-byte aligned (MXMOE_EINVAL).
+ * One launch, no workspace: calls on several streams may overlap. T = 0 is a no-op. */
+int rmsnorm_residual(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, const uint16_t* weight,
+                     float eps, int T, int H, uint16_t* sum_out, uint16_t* y, uint8_t* q, float* q_scale,
+                     const float* act_scale, void* stream);
+
 /* mxmoe_check -- synchronize `stream`, then read and clear the device error word.
  * Returns MXMOE_OK, MXMOE_EDEVICE (bad data seen by a kernel), MXMOE_ETIMEOUT (a bounded
  * device wait gave up) or MXMOE_ECUDA (the stream reported an error). */

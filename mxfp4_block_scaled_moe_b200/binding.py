@@ -40,6 +40,7 @@ _SIGS = {
     "moe_mxfp4_calibrate": [_vp] * 9 + [_i32] * 5 + [_vp, _vp],
     "moe_mxfp4_experts": [_vp, _vp, _i32, _i32, _i32, _i32] + [_vp] * 9,
     "moe_combine": [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp],
+    "rmsnorm_residual": [_vp, _i64, _vp, _i64, _vp, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "mxmoe_check": [_vp],
     "mxmoe_last_error": [],
     "mxmoe_last_launch_count": [],
@@ -352,6 +353,118 @@ def moe_combine(y, topk_idx, topk_w, inv, out=None, stream=None):
         out = torch.empty(T, H, dtype=torch.bfloat16, device=y.device)
     _call("moe_combine", _ptr(y), _ptr(topk_idx), _ptr(topk_w), _ptr(inv), T, H, k, _ptr(out), _stream(stream))
     return out
+
+
+# -------------------------------------------------------------- attention half -----
+
+# The checks below run on every call of operators whose kernels take a few microseconds, so
+# they are flat: one helper call per tensor, the message formed only on failure.
+
+def _device(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _refuse(t, dtype, shape, dev, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the other tensors on cuda:{dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t, dtype, shape, dev, name):
+    """Device pointer of a dense tensor of that type, shape and device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(t, dtype, shape, dev, name)
+    return t.data_ptr()
+
+
+def _dense_like(t, dtype):
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
+def _rows(t, H, dev, name):
+    """(device pointer, row stride) of a bf16 tensor (..., H) as rows: a dense tensor of any
+    rank, or two-dimensional rows cut from wider ones."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _refuse(t, torch.bfloat16, None, dev, name)
+    if t.is_contiguous():
+        return t.data_ptr(), H
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    return t.data_ptr(), t.stride(0)
+
+
+def _run_on(dev, stream, name, *args):
+    """_call with the tensors' device current; the stream goes last. Without a given stream
+    it is that device's current one."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _run_on(dev, stream, name, *args)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    L = _lib or lib()
+    rc = getattr(L, name)(*args, st)
+    if rc != OK:
+        raise MxmoeError(rc, name, L.mxmoe_last_error().decode(errors="replace"))
+
+
+def _norm(x, weight, residual, eps, sum_out, y, q, q_scale, act_scale, stream):
+    dev = _device(x, "x")
+    shape = x.shape
+    H = shape[-1]
+    px, ldx = _rows(x, H, dev, "x")
+    pr, ldr = None, H
+    if residual is not None:
+        if residual.shape != shape:
+            raise ValueError(f"residual must have x's shape {tuple(shape)}, got {tuple(residual.shape)}")
+        pr, ldr = _rows(residual, H, dev, "residual")
+    s = None if act_scale is None else ctypes.byref(ctypes.c_float(act_scale))
+    _run_on(dev, stream, "rmsnorm_residual", px, ldx, pr, ldr, _arg(weight, torch.bfloat16, (H,), dev, "weight"), eps,
+            x.numel() // H if H else 0, H, _arg(sum_out, torch.bfloat16, shape, dev, "sum_out"),
+            _arg(y, torch.bfloat16, shape, dev, "y"), _arg(q, torch.uint8, shape, dev, "q"),
+            None if q_scale is None else q_scale.data_ptr(), s)
+
+
+def _sum_out(x, residual, sum_out):
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out goes with a residual")
+    elif sum_out is None:
+        return _dense_like(x, torch.bfloat16)
+    return sum_out
+
+
+def rmsnorm_residual(x, weight, residual=None, eps=1e-5, sum_out=None, y=None, stream=None):
+    """(y, sum): h = bf16(x + residual) (x without one; sum is then None) and y = bf16(h *
+    weight / sqrt(mean(h^2) + eps)) over the last axis. sum_out may be `residual` (the
+    stream updated in place). Strided rows of a 2-D x or residual are taken as they are."""
+    sum_out = _sum_out(x, residual, sum_out)
+    if y is None:
+        y = _dense_like(x, torch.bfloat16)
+    _norm(x, weight, residual, eps, sum_out, y, None, None, None, stream)
+    return y, sum_out
+
+
+def rmsnorm_residual_fp8(x, weight, residual=None, eps=1e-5, act_scale=None, sum_out=None, q=None, y=None,
+                         stream=None):
+    """(q, scale, sum): as rmsnorm_residual with E4M3 codes (uint8) of the norm: divided by the
+    static act_scale (scale is then None), or by one scale per token, max|n| / 448 (scale:
+    fp32 of x's leading shape). y, if given, receives the bf16 norm too."""
+    sum_out = _sum_out(x, residual, sum_out)
+    if q is None:
+        q = _dense_like(x, torch.uint8)
+    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if act_scale is None else None
+    _norm(x, weight, residual, eps, sum_out, y, q, scale, act_scale, stream)
+    return q, scale, sum_out
 
 
 def mxmoe_check(stream=None):

@@ -1130,6 +1130,39 @@ int moe_mxfp4_calibrate(const uint16_t* x, const uint16_t* router_w, const uint1
   return run_layer(a, nullptr, nullptr, act_scale_out, static_cast<cudaStream_t>(stream));
 }
 
+int rmsnorm_residual(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, const uint16_t* weight,
+                     float eps, int T, int H, uint16_t* sum_out, uint16_t* y, uint8_t* q, float* q_scale,
+                     const float* act_scale, void* stream) {
+  t_last_error.clear();
+  t_last_launches = 0;
+  if (T < 0 || H <= 0) return fail(MXMOE_EINVAL, "T = %d must be >= 0 and H = %d positive", T, H);
+  if (H % 8) return fail(MXMOE_EALIGN, "H = %d is not a multiple of 8", H);
+  if (H > 32768) return fail(MXMOE_EUNSUPPORTED, "H = %d exceeds 32768", H);
+  if (ldx < H || ldx % 8 || (residual && (ldr < H || ldr % 8)))
+    return fail(MXMOE_EINVAL, "row strides must be multiples of 8 and at least H = %d", H);
+  if (!(eps >= 1e-12f && eps <= 1.0f)) return fail(MXMOE_EINVAL, "eps must lie in [1e-12, 1]");
+  if (act_scale && !(*act_scale >= 1e-30f && *act_scale <= 1e30f))
+    return fail(MXMOE_EINVAL, "act_scale must lie in [1e-30, 1e30]");
+  if (T == 0) return MXMOE_OK;   // an empty tensor's pointers may be null
+  if ((residual != nullptr) != (sum_out != nullptr))
+    return fail(MXMOE_EINVAL, "residual and sum_out go together");
+  if (!y && !q) return fail(MXMOE_EINVAL, "neither y nor q is asked for");
+  if (q ? (q_scale != nullptr) == (act_scale != nullptr) : (q_scale || act_scale))
+    return fail(MXMOE_EINVAL, "q needs act_scale (static) or q_scale (per token), and neither goes without q");
+  if (!x || !weight) return fail(MXMOE_EINVAL, "null pointer");
+  const void* ptrs[] = {x, residual, weight, sum_out, y, q, q_scale};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return fail(MXMOE_EINVAL, "every pointer must be 16-byte aligned");
+  Workspace* ws = nullptr;
+  if (int rc = current_device_ws(&ws)) return rc;
+  const mxmoe::NormArgs a{x, ldx, residual, ldr, weight, eps, act_scale ? *act_scale : 1.0f, T, H,
+                          sum_out, y, q, q_scale};
+  cudaError_t e = mxmoe::launch_rmsnorm(a, ws->sms, static_cast<cudaStream_t>(stream));
+  if (e) return cuda_fail(e, "rmsnorm launch");
+  t_last_launches = 1;
+  return MXMOE_OK;
+}
+
 int mxmoe_check(void* stream) {
   t_last_error.clear();
   Workspace* ws = nullptr;

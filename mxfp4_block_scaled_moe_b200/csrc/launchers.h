@@ -195,6 +195,23 @@ bool fp8_linear_supported();
 cudaError_t launch_fp8_linear(const uint8_t* xq, int T, int K, const uint8_t* wq, int N, float s, const float* bias,
                               uint16_t* out, float* part, int ksplit, int* err, int sms, cudaStream_t st);
 
+// residual addition + root-mean-square norm + FP8 cast (csrc/norm.cu): rows ldx / ldr elements
+// apart; residual with sum_out, y, q and q_scale nullable; q without q_scale uses s
+struct NormArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* residual;
+  int64_t ldr;
+  const uint16_t* weight;
+  float eps, s;
+  int T, H;
+  uint16_t* sum_out;
+  uint16_t* y;
+  uint8_t* q;
+  float* q_scale;
+};
+cudaError_t launch_rmsnorm(const NormArgs& a, int sms, cudaStream_t st);
+
 // mxmoe_tc_rate_probe: back-to-back kind::mxf8f6f4 MMAs (M = 128, N = n) on `ctas` CTAs
 cudaError_t launch_tc_rate(int n, int with_copy, int random, int iters, int ctas, int* err, cudaStream_t st);
 
