@@ -283,6 +283,54 @@ int rmsnorm_residual(const uint16_t* x, int64_t ldx, const uint16_t* residual, i
                      float eps, int T, int H, uint16_t* sum_out, uint16_t* y, uint8_t* q, float* q_scale,
                      const float* act_scale, void* stream);
 
+/* The paged MXFP4 key/value cache of mxfp4_kv_append and mxfp4_kv_attention ("quantization_
+ * mxfp4" (KerasFormers), Primitives, along the head dimension D): k_blocks, v_blocks: device
+ * uint8 (num_pages, Hkv, page_size, D/2); k_scales, v_scales: device uint8 (num_pages, Hkv,
+ * page_size, D/32). A token's place is its slot, page * page_size + offset. page_size is 16, 32,
+ * 64, 128 or 256 (MXMOE_EUNSUPPORTED otherwise). mxfp4_dequantize reads the arrays as they
+ * stand; a fresh cache needs no initialization.
+ *
+ * mxfp4_kv_append -- write the keys and values of T tokens: row t of k and v (device bf16, (Hkv,
+ * D) each, rows ldk / ldv elements apart: slices of a fused projection's output do) is
+ * quantized as mxfp4_quantize does (same bits for the same values) and stored at slots[t]
+ * (device int64). A negative slot skips its token (padding). A slot at or past num_pages *
+ * page_size is dropped and sets MXMOE_EDEVICE (see mxmoe_check). Distinct tokens have
+ * distinct slots: a slot given twice in one call is left with an unspecified mix of the two.
+ * Nothing but the given slots is written. D % 32 == 0 (MXMOE_EALIGN), D <= 1024; strides
+ * multiples of 8 and >= Hkv * D; every pointer 16-byte aligned. One launch, no workspace. */
+int mxfp4_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const int64_t* slots, int T,
+                    int Hkv, int D, uint8_t* k_blocks, uint8_t* k_scales, uint8_t* v_blocks, uint8_t* v_scales,
+                    int64_t num_pages, int page_size, void* stream);
+
+/* mxfp4_kv_attention -- attention of the last Lq tokens of B sequences over that cache, for
+ * decode (Lq = 1), drafted tokens and short prefill chunks. Query i of sequence b is token
+ * p = seq_lens[b] - Lq + i and sees the keys j <= p, with window > 0 only those with
+ * j > p - window (its own keys are in the cache already). For query head h, key/value head
+ * h / (Hq / Hkv):
+ *   z_j = scale * q . k_j,   out = sum_j e^{z_j} v_j / (sum_j e^{z_j} + e^{sinks[h]})
+ * (sinks: device fp32 (Hq), a logit without a value that joins each softmax; NULL: none). A
+ * query that sees no key gives zeros: seq_lens[b] = 0, or i < Lq - seq_lens[b].
+ * q: device bf16, token b * Lq + i at q + (b * Lq + i) * ldq, heads (Hq, D) dense; block_table:
+ * device int32 (B, max_pages), page n of sequence b holding its tokens [n page_size, (n + 1)
+ * page_size); entries that no query's keys need are not read (pages before the window may be
+ * gone). A needed page outside [0, num_pages) counts as unseen and sets MXMOE_EDEVICE, and so
+ * does a length past max_pages * page_size (cut to it). seq_lens: device int32 (B), negative
+ * counts as 0; the lengths stay on the device, so a captured call follows them. out: device
+ * bf16 (B, Lq, Hq, D). Cache places that no query sees may hold anything.
+ * Scores, maxima, sums and outputs are fp32 until the last rounding; weights are rounded to
+ * 11 bits (and to 2^-40 of a 32-column block's largest value scale) before the product with
+ * the values. Sums are joined in a fixed order: the same call gives the same bits.
+ * workspace: device memory of mxfp4_kv_attention_workspace's size, 16-byte aligned, the call's
+ * own until it has run (calls on two streams need two); it needs no initialization.
+ * Limits: D 64 or 128, Hq a multiple of Hkv, Hq <= 1024, Lq <= 128, B <= 65536, page sizes as
+ * above, window <= 2^30; ldq a multiple of 8. B = 0 is a no-op. Two launches. */
+int mxfp4_kv_attention_workspace(int B, int Lq, int Hq, int Hkv, int D, int64_t* bytes);
+int mxfp4_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* k_blocks, const uint8_t* k_scales,
+                       const uint8_t* v_blocks, const uint8_t* v_scales, int64_t num_pages, int page_size,
+                       const int32_t* block_table, int max_pages, const int32_t* seq_lens, const float* sinks, int B,
+                       int Lq, int Hq, int Hkv, int D, float scale, int window, uint16_t* out, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
 /* mxmoe_check -- synchronize `stream`, then read and clear the device error word.
  * Returns MXMOE_OK, MXMOE_EDEVICE (bad data seen by a kernel), MXMOE_ETIMEOUT (a bounded
  * device wait gave up) or MXMOE_ECUDA (the stream reported an error). */

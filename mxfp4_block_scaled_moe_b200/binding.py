@@ -8,6 +8,7 @@ bf16 tensors are passed as their bit patterns (torch.bfloat16 storage).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -41,6 +42,10 @@ _SIGS = {
     "moe_mxfp4_experts": [_vp, _vp, _i32, _i32, _i32, _i32] + [_vp] * 9,
     "moe_combine": [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp],
     "rmsnorm_residual": [_vp, _i64, _vp, _i64, _vp, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
+    "mxfp4_kv_append": [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _vp],
+    "mxfp4_kv_attention_workspace": [_i32, _i32, _i32, _i32, _i32, _vp],
+    "mxfp4_kv_attention": [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _i32, _vp, _vp] + [_i32] * 5
+                          + [_f32, _i32, _vp, _vp, _i64, _vp],
     "mxmoe_check": [_vp],
     "mxmoe_last_error": [],
     "mxmoe_last_launch_count": [],
@@ -404,20 +409,30 @@ def _rows(t, H, dev, name):
     return t.data_ptr(), t.stride(0)
 
 
-def _run_on(dev, stream, name, *args):
-    """_call with the tensors' device current; the stream goes last. Without a given stream
-    it is that device's current one."""
+def _run_on(dev, name, *args):
+    """_call with the tensors' device current; that device's current stream goes last."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _run_on(dev, stream, name, *args)
-    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+            return _run_on(dev, name, *args)
     L = _lib or lib()
-    rc = getattr(L, name)(*args, st)
+    rc = getattr(L, name)(*args, torch._C._cuda_getCurrentRawStream(dev))
     if rc != OK:
         raise MxmoeError(rc, name, L.mxmoe_last_error().decode(errors="replace"))
 
 
-def _norm(x, weight, residual, eps, sum_out, y, q, q_scale, act_scale, stream):
+def _on_stream(fn):
+    """Gives an operator its `stream` keyword: the call runs with that stream current, so
+    that the outputs and workspaces it makes belong to the stream that uses them."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _norm(x, weight, residual, eps, sum_out, y, q, q_scale, act_scale):
     dev = _device(x, "x")
     shape = x.shape
     H = shape[-1]
@@ -428,7 +443,7 @@ def _norm(x, weight, residual, eps, sum_out, y, q, q_scale, act_scale, stream):
             raise ValueError(f"residual must have x's shape {tuple(shape)}, got {tuple(residual.shape)}")
         pr, ldr = _rows(residual, H, dev, "residual")
     s = None if act_scale is None else ctypes.byref(ctypes.c_float(act_scale))
-    _run_on(dev, stream, "rmsnorm_residual", px, ldx, pr, ldr, _arg(weight, torch.bfloat16, (H,), dev, "weight"), eps,
+    _run_on(dev, "rmsnorm_residual", px, ldx, pr, ldr, _arg(weight, torch.bfloat16, (H,), dev, "weight"), eps,
             x.numel() // H if H else 0, H, _arg(sum_out, torch.bfloat16, shape, dev, "sum_out"),
             _arg(y, torch.bfloat16, shape, dev, "y"), _arg(q, torch.uint8, shape, dev, "q"),
             None if q_scale is None else q_scale.data_ptr(), s)
@@ -443,19 +458,20 @@ def _sum_out(x, residual, sum_out):
     return sum_out
 
 
-def rmsnorm_residual(x, weight, residual=None, eps=1e-5, sum_out=None, y=None, stream=None):
+@_on_stream
+def rmsnorm_residual(x, weight, residual=None, eps=1e-5, sum_out=None, y=None):
     """(y, sum): h = bf16(x + residual) (x without one; sum is then None) and y = bf16(h *
     weight / sqrt(mean(h^2) + eps)) over the last axis. sum_out may be `residual` (the
     stream updated in place). Strided rows of a 2-D x or residual are taken as they are."""
     sum_out = _sum_out(x, residual, sum_out)
     if y is None:
         y = _dense_like(x, torch.bfloat16)
-    _norm(x, weight, residual, eps, sum_out, y, None, None, None, stream)
+    _norm(x, weight, residual, eps, sum_out, y, None, None, None)
     return y, sum_out
 
 
-def rmsnorm_residual_fp8(x, weight, residual=None, eps=1e-5, act_scale=None, sum_out=None, q=None, y=None,
-                         stream=None):
+@_on_stream
+def rmsnorm_residual_fp8(x, weight, residual=None, eps=1e-5, act_scale=None, sum_out=None, q=None, y=None):
     """(q, scale, sum): as rmsnorm_residual with E4M3 codes (uint8) of the norm: divided by the
     static act_scale (scale is then None), or by one scale per token, max|n| / 448 (scale:
     fp32 of x's leading shape). y, if given, receives the bf16 norm too."""
@@ -463,8 +479,109 @@ def rmsnorm_residual_fp8(x, weight, residual=None, eps=1e-5, act_scale=None, sum
     if q is None:
         q = _dense_like(x, torch.uint8)
     scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if act_scale is None else None
-    _norm(x, weight, residual, eps, sum_out, y, q, scale, act_scale, stream)
+    _norm(x, weight, residual, eps, sum_out, y, q, scale, act_scale)
     return q, scale, sum_out
+
+
+def _cache(k_blocks, k_scales, v_blocks, v_scales, dev):
+    """(pointers, num_pages, Hkv, page_size, D) of a paged cache's four arrays."""
+    shape = k_blocks.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_blocks must be (num_pages, Hkv, page_size, D/2), got {tuple(shape)}")
+    sc = shape[:3] + (shape[3] // 16,)
+    ptrs = (_arg(k_blocks, torch.uint8, shape, dev, "k_blocks"), _arg(k_scales, torch.uint8, sc, dev, "k_scales"),
+            _arg(v_blocks, torch.uint8, shape, dev, "v_blocks"), _arg(v_scales, torch.uint8, sc, dev, "v_scales"))
+    return ptrs, shape[0], shape[1], shape[2], 2 * shape[3]
+
+
+def _tokens(t, dev, name):
+    """(device pointer, token stride) of a bf16 tensor (..., heads, D) whose heads are dense and
+    whose tokens are one stride apart."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _refuse(t, torch.bfloat16, None, dev, name)
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[-2] * t.shape[-1]
+    stride, shape = t.stride(), t.shape
+    if stride[-1] != 1 or stride[-2] != shape[-1]:
+        raise ValueError(f"{name}: each token's heads must be dense")
+    step = n = None
+    for size, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+        if size == 1:
+            continue
+        if step is None:
+            step, n = st, size
+        elif st != step * n:
+            raise ValueError(f"{name}: the tokens must be one stride apart")
+        else:
+            n *= size
+    return t.data_ptr(), shape[-2] * shape[-1] if step is None else step
+
+
+@_on_stream
+def mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales):
+    """Quantize the rows of k and v, bf16 (T, Hkv, D), to MXFP4 along D and write them to the
+    paged cache: blocks (num_pages, Hkv, page_size, D/2) and scales (num_pages, Hkv, page_size,
+    D/32), uint8. slots: int64 (T), page * page_size + offset; negative skips the token. k and
+    v may be slices of a fused projection's rows."""
+    dev = _device(k, "k")
+    ptrs, pages, Hkv, page_size, D = _cache(k_blocks, k_scales, v_blocks, v_scales, dev)
+    T = k.shape[0]
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
+        raise ValueError(f"k and v must be (T, {Hkv}, {D}), got {tuple(k.shape)} and {tuple(v.shape)}")
+    pk, ldk = _tokens(k, dev, "k")
+    pv, ldv = _tokens(v, dev, "v")
+    _run_on(dev, "mxfp4_kv_append", pk, ldk, pv, ldv, _arg(slots, torch.int64, (T,), dev, "slots"), T, Hkv, D, *ptrs,
+            pages, page_size)
+
+
+_attention_bytes: dict = {}
+
+
+def mxfp4_kv_attention_workspace(B, Lq, Hq, Hkv, D, device=None) -> int:
+    """Bytes of workspace that mxfp4_kv_attention needs for these sizes."""
+    dev = torch.device("cuda" if device is None else device).index
+    dev = torch.cuda.current_device() if dev is None else dev
+    key = (dev, B, Lq, Hq, Hkv, D)
+    if key not in _attention_bytes:
+        n = ctypes.c_int64(0)
+        with torch.cuda.device(dev):
+            _call("mxfp4_kv_attention_workspace", B, Lq, Hq, Hkv, D, ctypes.byref(n))
+        _attention_bytes[key] = n.value
+    return _attention_bytes[key]
+
+
+@_on_stream
+def mxfp4_kv_attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, seq_lens, scale=None, window=0, sinks=None,
+                       out=None, workspace=None):
+    """Attention of q, bf16 (B, Lq, Hq, D) or (B, Hq, D), the last Lq tokens of B sequences, over
+    the paged MXFP4 cache; returns bf16 of q's shape. block_table: int32 (B, max_pages);
+    seq_lens: int32 (B), the new tokens included; scale: 1 / sqrt(D) unless given; window: the
+    keys a query sees, itself included (0: all); sinks: fp32 (Hq) logits joining each softmax.
+    q's tokens may be slices of a fused projection's rows. workspace: uint8 of at least
+    mxfp4_kv_attention_workspace's size, made by the call unless given."""
+    dev = _device(q, "q")
+    ptrs, pages, Hkv, page_size, D = _cache(k_blocks, k_scales, v_blocks, v_scales, dev)
+    shape = q.shape
+    if len(shape) not in (3, 4) or shape[-1] != D:
+        raise ValueError(f"q must be (B, Lq, Hq, {D}) or (B, Hq, {D}), got {tuple(shape)}")
+    B, Hq = shape[0], shape[-2]
+    Lq = shape[1] if len(shape) == 4 else 1
+    pq, ldq = _tokens(q, dev, "q")
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must be (B, max_pages), got {tuple(block_table.shape)}")
+    max_pages = block_table.shape[1]
+    if out is None:
+        out = _dense_like(q, torch.bfloat16)
+    if workspace is None:
+        key = (dev, B, Lq, Hq, Hkv, D)
+        n = _attention_bytes.get(key) or mxfp4_kv_attention_workspace(B, Lq, Hq, Hkv, D, q.device)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _run_on(dev, "mxfp4_kv_attention", pq, ldq, *ptrs, pages, page_size,
+            _arg(block_table, torch.int32, (B, max_pages), dev, "block_table"), max_pages,
+            _arg(seq_lens, torch.int32, (B,), dev, "seq_lens"), _arg(sinks, torch.float32, (Hq,), dev, "sinks"), B, Lq,
+            Hq, Hkv, D, D ** -0.5 if scale is None else scale, window, _arg(out, torch.bfloat16, shape, dev, "out"),
+            _arg(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel())
+    return out
 
 
 def mxmoe_check(stream=None):

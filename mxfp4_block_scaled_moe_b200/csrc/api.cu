@@ -1163,6 +1163,123 @@ int rmsnorm_residual(const uint16_t* x, int64_t ldx, const uint16_t* residual, i
   return MXMOE_OK;
 }
 
+// log2 of a cache's page size, or -1 if it is none of 16, 32, 64, 128, 256
+static int page_shift_of(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+int mxfp4_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const int64_t* slots, int T,
+                    int Hkv, int D, uint8_t* k_blocks, uint8_t* k_scales, uint8_t* v_blocks, uint8_t* v_scales,
+                    int64_t num_pages, int page_size, void* stream) {
+  t_last_error.clear();
+  t_last_launches = 0;
+  if (T < 0 || Hkv <= 0 || D <= 0 || num_pages < 0)
+    return fail(MXMOE_EINVAL, "T = %d and num_pages must be >= 0, Hkv = %d and D = %d positive", T, Hkv, D);
+  if (D % 32) return fail(MXMOE_EALIGN, "D = %d is not a multiple of 32 (MXFP4 block size)", D);
+  if (T >= (1 << 24) || Hkv > 1024 || D > 1024 || num_pages >= (1ll << 31))
+    return fail(MXMOE_EUNSUPPORTED, "T < 2^24, Hkv <= 1024, D <= 1024 and num_pages < 2^31 are supported");
+  const int shift = page_shift_of(page_size);
+  if (shift < 0) return fail(MXMOE_EUNSUPPORTED, "page_size = %d is not 16, 32, 64, 128 or 256", page_size);
+  if (T == 0) return MXMOE_OK;
+  const int64_t row = static_cast<int64_t>(Hkv) * D;
+  if (ldk < row || ldv < row || ldk % 8 || ldv % 8)
+    return fail(MXMOE_EINVAL, "row strides must be multiples of 8 and at least Hkv * D = %lld", (long long)row);
+  if (!k || !v || !slots || (num_pages > 0 && (!k_blocks || !k_scales || !v_blocks || !v_scales)))
+    return fail(MXMOE_EINVAL, "null pointer");
+  const void* ptrs[] = {k, v, slots, k_blocks, k_scales, v_blocks, v_scales};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return fail(MXMOE_EINVAL, "every pointer must be 16-byte aligned");
+  Workspace* ws = nullptr;
+  if (int rc = current_device_ws(&ws)) return rc;
+  const mxmoe::KvAppendArgs a{k, v, ldk, ldv, slots, num_pages << shift, T, Hkv, D, shift,
+                              k_blocks, k_scales, v_blocks, v_scales, ws->err};
+  cudaError_t e = mxmoe::launch_kv_append(a, static_cast<cudaStream_t>(stream));
+  if (e) return cuda_fail(e, "kv append launch");
+  t_last_launches = 1;
+  return MXMOE_OK;
+}
+
+static int check_kv_attention_shape(int B, int Lq, int Hq, int Hkv, int D) {
+  if (B < 0 || Lq <= 0 || Hq <= 0 || Hkv <= 0)
+    return fail(MXMOE_EINVAL, "B = %d must be >= 0, Lq = %d, Hq = %d and Hkv = %d positive", B, Lq, Hq, Hkv);
+  if (D != 64 && D != 128) return fail(MXMOE_EUNSUPPORTED, "D = %d is neither 64 nor 128", D);
+  if (Hq % Hkv) return fail(MXMOE_EINVAL, "Hq = %d is not a multiple of Hkv = %d", Hq, Hkv);
+  if (B > 65536 || Lq > 128 || Hq > 1024)
+    return fail(MXMOE_EUNSUPPORTED, "B <= 65536, Lq <= 128 and Hq <= 1024 are supported");
+  return MXMOE_OK;
+}
+
+int mxfp4_kv_attention_workspace(int B, int Lq, int Hq, int Hkv, int D, int64_t* bytes) {
+  t_last_error.clear();
+  if (int rc = check_kv_attention_shape(B, Lq, Hq, Hkv, D)) return rc;
+  if (!bytes) return fail(MXMOE_EINVAL, "bytes is NULL");
+  Workspace* ws = nullptr;
+  if (int rc = current_device_ws(&ws)) return rc;
+  *bytes = static_cast<int64_t>(mxmoe::kv_attention_workspace(B, Lq, Hq, Hkv, D, ws->sms));
+  return MXMOE_OK;
+}
+
+int mxfp4_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* k_blocks, const uint8_t* k_scales,
+                       const uint8_t* v_blocks, const uint8_t* v_scales, int64_t num_pages, int page_size,
+                       const int32_t* block_table, int max_pages, const int32_t* seq_lens, const float* sinks, int B,
+                       int Lq, int Hq, int Hkv, int D, float scale, int window, uint16_t* out, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  t_last_error.clear();
+  t_last_launches = 0;
+  if (int rc = check_kv_attention_shape(B, Lq, Hq, Hkv, D)) return rc;
+  if (num_pages < 0 || max_pages < 0) return fail(MXMOE_EINVAL, "num_pages and max_pages must be >= 0");
+  if (num_pages >= (1ll << 31) || max_pages > (1 << 24))
+    return fail(MXMOE_EUNSUPPORTED, "num_pages < 2^31 and max_pages <= 2^24 are supported");
+  const int shift = page_shift_of(page_size);
+  if (shift < 0) return fail(MXMOE_EUNSUPPORTED, "page_size = %d is not 16, 32, 64, 128 or 256", page_size);
+  if (window < 0) return fail(MXMOE_EINVAL, "window = %d is negative", window);
+  if (window > (1 << 30)) return fail(MXMOE_EUNSUPPORTED, "window = %d exceeds 2^30", window);
+  if (!(scale >= -1e30f && scale <= 1e30f)) return fail(MXMOE_EINVAL, "scale must be finite (at most 1e30)");
+  if (B == 0) return MXMOE_OK;
+  if (ldq < static_cast<int64_t>(Hq) * D || ldq % 8)
+    return fail(MXMOE_EINVAL, "ldq must be a multiple of 8 and at least Hq * D = %lld", (long long)Hq * D);
+  if (!q || !seq_lens || !out || !workspace || (max_pages > 0 && !block_table) ||
+      (num_pages > 0 && (!k_blocks || !k_scales || !v_blocks || !v_scales)))
+    return fail(MXMOE_EINVAL, "null pointer");
+  const void* ptrs[] = {q, k_blocks, k_scales, v_blocks, v_scales, block_table, seq_lens, sinks, out, workspace};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return fail(MXMOE_EINVAL, "every pointer must be 16-byte aligned");
+  Workspace* ws = nullptr;
+  if (int rc = current_device_ws(&ws)) return rc;
+  const size_t need = mxmoe::kv_attention_workspace(B, Lq, Hq, Hkv, D, ws->sms);
+  if (workspace_bytes < static_cast<int64_t>(need))
+    return fail(MXMOE_EINVAL, "workspace of %lld bytes, %zu needed", (long long)workspace_bytes, need);
+  mxmoe::KvAttentionArgs a{};
+  a.q = q;
+  a.q_stride = ldq;
+  a.k_blocks = k_blocks;
+  a.k_scales = k_scales;
+  a.v_blocks = v_blocks;
+  a.v_scales = v_scales;
+  a.num_pages = static_cast<int>(num_pages);
+  a.page_shift = shift;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.max_pages = max_pages;
+  a.sinks = sinks;
+  a.B = B;
+  a.Lq = Lq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.D = D;
+  a.R = a.G * Lq;
+  a.window = window;
+  a.scale_log2 = scale * 1.44269504088896f;
+  a.out = out;
+  a.err = ws->err;
+  cudaError_t e = mxmoe::launch_kv_attention(a, workspace, ws->sms, static_cast<cudaStream_t>(stream));
+  if (e) return cuda_fail(e, "kv attention launch");
+  t_last_launches = 2;
+  return MXMOE_OK;
+}
+
 int mxmoe_check(void* stream) {
   t_last_error.clear();
   Workspace* ws = nullptr;

@@ -212,6 +212,50 @@ struct NormArgs {
 };
 cudaError_t launch_rmsnorm(const NormArgs& a, int sms, cudaStream_t st);
 
+// append to a paged MXFP4 key/value cache (csrc/kv_append.cu); rows ldk / ldv elements apart
+struct KvAppendArgs {
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t ldk, ldv;
+  const int64_t* slots;
+  int64_t num_slots;
+  int T, Hkv, D, page_shift;
+  uint8_t* k_blocks;
+  uint8_t* k_scales;
+  uint8_t* v_blocks;
+  uint8_t* v_scales;
+  int* err;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
+
+// attention over that cache (csrc/kv_attention.cu): D 64 or 128. launch_kv_attention sets RT
+// and the workspace pointers.
+struct KvAttentionArgs {
+  const uint16_t* q;
+  int64_t q_stride;             // elements between tokens
+  const uint8_t* k_blocks;
+  const uint8_t* k_scales;
+  const uint8_t* v_blocks;
+  const uint8_t* v_scales;
+  int num_pages, page_shift;
+  const int32_t* block_table;   // (B, max_pages)
+  const int32_t* seq_lens;      // (B)
+  int max_pages;
+  const float* sinks;           // (Hkv * G) or null
+  int B, Lq, Hkv, G, D;
+  int R;                        // G * Lq rows share a key/value head's keys
+  int window;                   // 0: none
+  float scale_log2;             // softmax scale * log2(e)
+  uint16_t* out;                // (B, Lq, Hkv * G, D)
+  int* err;
+  int RT;                       // row tiles of an item
+  int4* desc;
+  float2* part_ml;
+  float* part;
+};
+size_t kv_attention_workspace(int B, int Lq, int Hq, int Hkv, int D, int sms);
+cudaError_t launch_kv_attention(KvAttentionArgs a, void* workspace, int sms, cudaStream_t st);
+
 // mxmoe_tc_rate_probe: back-to-back kind::mxf8f6f4 MMAs (M = 128, N = n) on `ctas` CTAs
 cudaError_t launch_tc_rate(int n, int with_copy, int random, int iters, int ctas, int* err, cudaStream_t st);
 

@@ -53,3 +53,46 @@ def test_norm_argument_checks(L):
     for k in ("x", "res", "w", "so", "y"):
         assert _norm(L, **{k: MIS}) == EINVAL and "aligned" in err(L)
     assert _norm(L, q=A, qs=MIS) == EINVAL
+
+
+def _append(L, k=A, ldk=128, v=A, ldv=128, slots=A, T=4, Hkv=2, D=64, kb=A, ks=A, vb=A, vs=A, pages=3, page=16):
+    return L.mxfp4_kv_append(k, ldk, v, ldv, slots, T, Hkv, D, kb, ks, vb, vs, pages, page, None)
+
+
+def test_kv_append_argument_checks(L):
+    assert _append(L, T=0) == OK and _append(L, T=0, k=None, slots=None) == OK
+    assert _append(L, T=-1) == EINVAL and _append(L, Hkv=0) == EINVAL and _append(L, D=0) == EINVAL
+    assert _append(L, D=48) == EALIGN and "multiple of 32" in err(L)
+    for page in (0, 8, 24, 512, -16):
+        assert _append(L, page=page) == EUNSUPPORTED and "page_size" in err(L)
+    assert _append(L, ldk=120) == EINVAL and _append(L, ldv=132) == EINVAL
+    for n in ("k", "v", "slots", "kb", "ks", "vb", "vs"):
+        assert _append(L, **{n: None}) == EINVAL
+        assert _append(L, **{n: MIS}) == EINVAL and "aligned" in err(L)
+    assert _append(L, pages=-1) == EINVAL and _append(L, pages=1 << 31) == EUNSUPPORTED
+
+
+def _attend(L, q=A, ldq=512, kb=A, ks=A, vb=A, vs=A, pages=3, page=16, table=A, width=2, lens=A, sinks=None, B=2, Lq=1,
+            Hq=8, Hkv=2, D=64, scale=0.125, window=0, out=A, ws=A, nbytes=0):
+    return L.mxfp4_kv_attention(q, ldq, kb, ks, vb, vs, pages, page, table, width, lens, sinks, B, Lq, Hq, Hkv, D, scale,
+                                window, out, ws, nbytes, None)
+
+
+def test_kv_attention_argument_checks(L):
+    assert _attend(L, B=0) == OK and _attend(L, B=0, q=None, lens=None, out=None, ws=None) == OK
+    assert _attend(L, B=-1) == EINVAL and _attend(L, Lq=0) == EINVAL and _attend(L, Hkv=0) == EINVAL
+    assert _attend(L, Hq=9) == EINVAL and "multiple of Hkv" in err(L)
+    for D in (32, 96, 256):
+        assert _attend(L, D=D) == EUNSUPPORTED
+    assert _attend(L, Lq=129) == EUNSUPPORTED and _attend(L, Hq=2048) == EUNSUPPORTED and _attend(L, B=65537) == EUNSUPPORTED
+    assert _attend(L, page=48) == EUNSUPPORTED and _attend(L, window=-1) == EINVAL
+    assert _attend(L, window=(1 << 30) + 1) == EUNSUPPORTED
+    assert _attend(L, scale=float("nan")) == EINVAL and _attend(L, scale=float("inf")) == EINVAL
+    assert _attend(L, ldq=504) == EINVAL and _attend(L, ldq=516) == EINVAL
+    for n in ("q", "kb", "ks", "vb", "vs", "table", "lens", "out", "ws"):
+        assert _attend(L, **{n: None}) == EINVAL
+        assert _attend(L, **{n: MIS}) == EINVAL and "aligned" in err(L)
+    assert _attend(L, sinks=MIS) == EINVAL
+    n = ctypes.c_int64(0)
+    assert L.mxfp4_kv_attention_workspace(2, 1, 8, 2, 96, ctypes.byref(n)) == EUNSUPPORTED
+    assert L.mxfp4_kv_attention_workspace(2, 1, 8, 2, 64, None) == EINVAL
