@@ -11,8 +11,8 @@
 //    64/128-row tiles would be mostly padding and would need the codes expanded through
 //    shared memory. A key's e2m1 codes are exact in f16; its block scale multiplies the fp32
 //    block sum instead of 32 values. Queries enter as f16 after an exact power-of-two shift
-//    per row and 32-value block (largest magnitude to [2^14, 2^15): bf16's 8 bits survive down
-//    to 2^-29 of the block's largest).
+//    per row (largest magnitude to [2^14, 2^15): bf16's 8 bits survive down to 2^-29 of the
+//    row's largest, some of them to 2^-39).
 //  - O^T += V^T P^T: the value scales multiply the weights, p 2^(e_j - E + 15), where E is the
 //    largest value exponent seen so far in that 32-value block; the weights are then rounded
 //    to f16 (11 bits; absolute floor 2^-40 of the largest scale). Maximum, sum, and all
@@ -20,12 +20,13 @@
 // Row maxima, sums and E stay with the warp and its accumulators are rescaled only in units
 // where one of them grows.
 //
-// Work split: 32-key units of all (sequence, key/value head, row tile) items in one line; each
-// CTA takes an equal run of them whatever the sequences' lengths (the lengths are on the
-// device, so every CTA finds its run by itself), its warps take units in turn through private
-// cp.async rings, without barriers between them, and join at an item's end. An item that ends
-// up in several CTAs leaves fp32 partials in the caller's workspace, joined in CTA order by a
-// second small kernel: nothing in the result depends on timing, and no counter outlives a call.
+// Work split: 32-key units of all (sequence, key/value head, row tile) items in one line; every
+// warp of the grid takes an equal run of them whatever the sequences' lengths (the lengths are
+// on the device, so each CTA finds its warps' runs by itself) and streams it through a private
+// cp.async ring, without a barrier after the start. A warp writes the items that lie wholly in
+// its run; of the others it leaves fp32 partials in the caller's workspace, joined in run order
+// by a second small kernel: nothing in the result depends on timing, and no counter outlives a
+// call.
 #include <algorithm>
 
 #include "common.cuh"
@@ -37,8 +38,8 @@ namespace kva {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 32;          // keys per unit
-constexpr int kMinUnits = 8;       // least units of a CTA's run: one per warp
-constexpr int kCombineThreads = 256;
+constexpr int kMinUnits = 2;       // least units of a warp's run
+constexpr int kJoinThreads = 256;
 
 template <int D, int NT>
 struct Shape {
@@ -48,9 +49,9 @@ struct Shape {
   static constexpr int kKV = kUnit * kRowBytes;        // bytes of a unit's keys (or values)
   static constexpr int kSc = kUnit * kBlocks;          // their scales
   static constexpr int kStageBytes = 2 * kKV + 2 * kSc + 16;
-  static constexpr int kStages = D == 64 ? 4 : 2;
-  static constexpr int kJoinBytes = 2 * kWarps * kRows * 32 * 4;   // two 32-column slabs of every warp's rows
-  static constexpr int kSmem = kWarps * kStages * kStageBytes + kJoinBytes;
+  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kSmem = kWarps * kStages * kStageBytes;
+  static constexpr int kCtas = D == 64 || NT == 1 ? 2 : 1;   // per SM, by registers
 };
 
 // ------------------------------------------------------------------ small pieces ---
@@ -75,6 +76,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -87,6 +94,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
@@ -96,8 +108,24 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-// e8m0 byte to fp32 (255 reads as infinity, 0 as 2^-127)
-__device__ __forceinline__ float scale_f32(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+// the scale bytes of a key's blocks (2 or 4 of them), at `at`
+template <int kBlocks>
+__device__ __forceinline__ uint32_t lds_scales(uint32_t at) {
+  if constexpr (kBlocks == 4) return lds32(at);
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(at) : "memory");
+  return v;
+}
+// byte k of a word as the exponent field of an fp32: 2^(byte - 127). Byte 0 reads as zero: its
+// block's values are below 2^-124.
+__device__ __forceinline__ uint32_t exponent_of(uint32_t word, int k) {
+  return (k < 3 ? word << (23 - 8 * k) : word >> 1) & 0x7F800000u;
+}
 
 // ------------------------------------------------------------------- work line -----
 __device__ __forceinline__ int seq_len(const KvAttentionArgs& p, int b) {
@@ -110,64 +138,63 @@ __device__ __forceinline__ int seq_len(const KvAttentionArgs& p, int b) {
   return max(n, 0);
 }
 
-// first key of a sequence's units: the first that its first query sees, rounded down to a unit
-__device__ __forceinline__ int first_key(const KvAttentionArgs& p, int len) {
-  return p.window > 0 ? max(0, len - p.Lq + 1 - p.window) & ~(kUnit - 1) : 0;
+// the first key that a sequence's first query sees
+__device__ __forceinline__ int first_seen(const KvAttentionArgs& p, int len) {
+  return p.window > 0 ? max(0, len - p.Lq + 1 - p.window) : 0;
 }
 
 __device__ __forceinline__ int units_of(const KvAttentionArgs& p, int len) {
-  return max(1, (len - first_key(p, len) + kUnit - 1) / kUnit);   // an empty sequence still writes its zeros
+  const int first = first_seen(p, len) & ~(kUnit - 1);
+  return max(1, (len - first + kUnit - 1) / kUnit);   // an empty sequence still writes its zeros
 }
 
-// Position in the line of units: item j (key/value head and row tile) of sequence b.
+// Position in the line of units: an item (key/value head h, row tile rt of sequence b), its
+// first unit relative to the warp's run, its units.
 struct Cursor {
-  int b, j, len, first, units;
-  int64_t start;   // of the item
+  int b, h, rt, len, units, start;
   __device__ void load(const KvAttentionArgs& p) {
     len = seq_len(p, b);
-    first = first_key(p, len);
     units = units_of(p, len);
   }
-  __device__ void next(const KvAttentionArgs& p, int per_seq) {
+  __device__ void next(const KvAttentionArgs& p) {
     start += units;
-    if (++j == per_seq) {
-      j = 0;
-      if (++b < p.B) load(p);
-    }
+    if (++rt < p.RT) return;
+    rt = 0;
+    if (++h < p.Hkv) return;
+    h = 0;
+    if (++b < p.B) load(p);
   }
 };
 
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* buf) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) v += buf[w];
-  __syncthreads();
-  return v;
-}
-
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, (D == 64 || NT == 1) ? 2 : 1) kv_attention_kernel(const KvAttentionArgs p) {
+__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_kernel(const KvAttentionArgs p) {
   using S = Shape<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 s_ml[kWarps][S::kRows];
   __shared__ int64_t s_sum[kWarps];
-  __shared__ int s_b;
-  __shared__ int64_t s_base;
+  __shared__ int64_t s_pre[kThreads];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int per_seq = p.Hkv * p.RT;
   griddep_launch_dependents();   // the joining kernel may take its places; it waits for this one's end
 
-  // ---- this CTA's run of units [t0, t1) of n ----
-  int64_t mine = 0;
-  for (int b = threadIdx.x; b < p.B; b += kThreads) mine += units_of(p, seq_len(p, b));
-  const int64_t n = block_sum(mine, s_sum) * per_seq;
-  const int64_t per = max(static_cast<int64_t>(kMinUnits), (n + gridDim.x - 1) / gridDim.x);
-  const int64_t t0 = per * blockIdx.x, t1 = min(n, t0 + per);
-  if (t0 >= n) return;
+  // ---- this warp's run: units [t0, t0 + count) of n ----
+  int64_t n = 0;
+  for (int b = threadIdx.x; b < p.B; b += kThreads) n += units_of(p, seq_len(p, b));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  if (lane == 0) s_sum[warp] = n;
+  __syncthreads();
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) n += s_sum[w];
+  n *= per_seq;
+  const int64_t runs = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t per = max(static_cast<int64_t>(kMinUnits), (n + runs - 1) / runs);
+  // neighbouring runs go to different SMs, so that a short line still uses all of them
+  const int run = warp * gridDim.x + blockIdx.x;
+  const int64_t t0 = per * run;
+  const int count = static_cast<int>(max(static_cast<int64_t>(0), min(per, n - t0)));
+  Cursor cur;
+  cur.b = -1;
   {
     int64_t base = 0;   // units before this chunk of sequences
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -179,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, (D == 64 || NT == 1) ? 2 : 1) kv_att
         const int64_t x = __shfl_up_sync(0xffffffffu, pre, o);
         if (lane >= o) pre += x;
       }
+      __syncthreads();   // s_sum and s_pre of the step before have been read
       if (lane == 31) s_sum[warp] = pre;
       __syncthreads();
       int64_t all = 0;
@@ -187,83 +215,87 @@ __global__ void __launch_bounds__(kThreads, (D == 64 || NT == 1) ? 2 : 1) kv_att
         if (w < warp) pre += s_sum[w];
         all += s_sum[w];
       }
-      const int64_t from = base + pre - u;
-      if (u > 0 && from <= t0 && t0 < from + u) {
-        s_b = b;
-        s_base = from;
+      s_pre[threadIdx.x] = base + pre;
+      __syncthreads();
+      if (count > 0 && base <= t0 && t0 < base + all) {
+        // the first sequence of the chunk whose units end after t0
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+          const unsigned past = __ballot_sync(0xffffffffu, s_pre[32 * i + lane] > t0);
+          if (past && cur.b < 0) {
+            const int at = 32 * i + __ffs(past) - 1;
+            cur.b = b0 + at;
+            cur.load(p);
+            const int64_t from = s_pre[at] - static_cast<int64_t>(cur.units) * per_seq;
+            const int j = static_cast<int>((t0 - from) / cur.units);
+            cur.h = j / p.RT;
+            cur.rt = j % p.RT;
+            cur.start = static_cast<int>(from + static_cast<int64_t>(j) * cur.units - t0);
+          }
+        }
       }
       base += all;
-      __syncthreads();
-      if (t0 < base) break;
     }
   }
-  Cursor cur;
-  cur.b = s_b;
-  cur.load(p);
-  cur.j = static_cast<int>((t0 - s_base) / cur.units);
-  cur.start = s_base + static_cast<int64_t>(cur.j) * cur.units;
+  if (count == 0) return;
 
   // ---- this warp's ring of units ----
-  uint8_t* ring = smem + warp * S::kStages * S::kStageBytes;
-  const uint32_t ring_u32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  float* join = reinterpret_cast<float*>(smem + kWarps * S::kStages * S::kStageBytes);
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::kStages * S::kStageBytes;
+  constexpr int kPages = 2 * S::kKV + 2 * S::kSc;   // offset of a stage's flags: which 16 keys were loaded
+  constexpr int kChunks = S::kRowBytes / 16;        // 16-byte chunks of a row, one MXFP4 block each
+  constexpr int kLoads = S::kKV / 512;              // of a unit's keys, per lane; half of them for each 16 keys
+  constexpr int kScChunks = S::kSc / 16;
+  // A row's chunks are permuted so that the eight rows of an operand load fall in different
+  // banks; the permutation of a key repeats every 8 keys.
+  const uint32_t put = (lane / kChunks) * S::kRowBytes +
+                       16 * ((lane % kChunks) ^ (kChunks == 2 ? (lane >> 3) & 1 : (lane >> 3) & 3));
+  const int64_t page_rows = static_cast<int64_t>(p.Hkv) << p.page_shift;
+  const int in_page = (1 << p.page_shift) - 1;
 
   Cursor in = cur;           // of the next unit to load
-  int64_t in_unit = t0 + warp;
-  int pid0 = 0, pid1 = 0, in_key = 0;
+  int in_unit = 0, in_key = 0, pid0 = 0, pid1 = 0;
   bool in_load0 = false, in_load1 = false;
   // looks up the pages of unit in_unit (16 keys from each: a page holds 16 keys or more)
   auto look = [&]() {
-    if (in_unit >= t1) return;
-    while (in_unit >= in.start + in.units) in.next(p, per_seq);
-    in_key = in.first + kUnit * static_cast<int>(in_unit - in.start);
-    const int lo = p.window > 0 ? max(0, in.len - p.Lq + 1 - p.window) : 0;   // keys that no query sees need no page
+    if (in_unit >= count) return;
+    if (in_unit >= in.start + in.units) in.next(p);
+    const int lo = first_seen(p, in.len);   // keys that no query sees need no page
+    in_key = (lo & ~(kUnit - 1)) + kUnit * (in_unit - in.start);
     in_load0 = in_key < in.len && in_key + 16 > lo;
     in_load1 = in_key + 16 < in.len && in_key + 32 > lo;
     const int32_t* row = p.block_table + static_cast<int64_t>(in.b) * p.max_pages;
     if (in_load0) pid0 = __ldg(row + (in_key >> p.page_shift));
     if (in_load1) pid1 = __ldg(row + ((in_key + 16) >> p.page_shift));
   };
+  auto load16 = [&](uint32_t dst, int pid, int key, int second) {
+    const int64_t row = pid * page_rows + ((in.h << p.page_shift) + (key & in_page));
+    const uint8_t* k = p.k_blocks + row * S::kRowBytes + 16 * lane;
+    const uint8_t* v = p.v_blocks + row * S::kRowBytes + 16 * lane;
+#pragma unroll
+    for (int i = 0; i < kLoads / 2; ++i) {
+      cp_async16(dst + put + 512 * (i + second * (kLoads / 2)), k + 512 * i);
+      cp_async16(dst + put + 512 * (i + second * (kLoads / 2)) + S::kKV, v + 512 * i);
+    }
+    // 16 keys' scales: half of the chunks of keys, half of those of values
+    if (lane < kScChunks) {
+      const bool val = lane >= kScChunks / 2;
+      const int c = lane % (kScChunks / 2);
+      cp_async16(dst + 2 * S::kKV + (val ? S::kSc : 0) + second * (S::kSc / 2) + 16 * c,
+                 (val ? p.v_scales : p.k_scales) + row * S::kBlocks + 16 * c);
+    }
+  };
   auto issue = [&](int stage) {
-    if (in_unit < t1) {
-      const uint32_t dst = ring_u32 + stage * S::kStageBytes;
+    if (in_unit < count) {
+      const uint32_t dst = ring + stage * S::kStageBytes;
       const bool ok0 = in_load0 && static_cast<uint32_t>(pid0) < static_cast<uint32_t>(p.num_pages);
       const bool ok1 = in_load1 && static_cast<uint32_t>(pid1) < static_cast<uint32_t>(p.num_pages);
+      if (ok0) load16(dst, pid0, in_key, 0);
+      if (ok1) load16(dst, pid1, in_key + 16, 1);
       if (lane == 0) {
         if (ok0 != in_load0 || ok1 != in_load1) set_device_error(p.err, MXMOE_EDEVICE);   // a page outside the cache
-        *reinterpret_cast<int*>(ring + stage * S::kStageBytes + 2 * S::kKV + 2 * S::kSc) = (ok0 ? 1 : 0) | (ok1 ? 2 : 0);
+        asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(dst + kPages), "r"((ok0 ? 1 : 0) | (ok1 ? 2 : 0)) : "memory");
       }
-      const int h = in.j / p.RT;
-      const int in_page = in_key & ((1 << p.page_shift) - 1);
-      const int in_page1 = (in_key + 16) & ((1 << p.page_shift) - 1);
-      // cache rows of the unit's first and second 16 keys
-      const int64_t r0 = ((static_cast<int64_t>(pid0) * p.Hkv + h) << p.page_shift) + in_page;
-      const int64_t r1 = ((static_cast<int64_t>(pid1) * p.Hkv + h) << p.page_shift) + in_page1 - 16;
-      constexpr int kChunks = S::kRowBytes / 16;   // 16-byte chunks of a row, one MXFP4 block each
-#pragma unroll
-      for (int i = 0; i < S::kKV / 512; ++i) {
-        const int c = 32 * i + lane, key = c / kChunks, blk = c % kChunks;
-        const bool second = key >= 16;
-        if (second ? ok1 : ok0) {
-          const int64_t off = ((second ? r1 : r0) + key) * S::kRowBytes + 16 * blk;
-          // a row's chunks are permuted so that the eight rows of an operand load fall in
-          // different banks
-          const int sw = kChunks == 2 ? blk ^ ((key >> 2) & 1) : blk ^ ((key >> 1) & 3);
-          const uint32_t at = dst + key * S::kRowBytes + 16 * sw;
-          cp_async16(at, p.k_blocks + off);
-          cp_async16(at + S::kKV, p.v_blocks + off);
-        }
-      }
-      constexpr int kScChunks = S::kSc / 16, kScKeys = kUnit / kScChunks;   // keys of a 16-byte chunk of scales
-      if (lane < 2 * kScChunks) {
-        const bool val = lane >= kScChunks;
-        const int key = (lane % kScChunks) * kScKeys;
-        const bool second = key >= 16;
-        if (second ? ok1 : ok0)
-          cp_async16(dst + 2 * S::kKV + lane * 16,
-                     (val ? p.v_scales : p.k_scales) + ((second ? r1 : r0) + key) * S::kBlocks);
-      }
-      in_unit += kWarps;
+      ++in_unit;
     }
     cp_async_commit();
     look();
@@ -272,57 +304,57 @@ __global__ void __launch_bounds__(kThreads, (D == 64 || NT == 1) ? 2 : 1) kv_att
 #pragma unroll
   for (int s = 0; s < S::kStages - 1; ++s) issue(s);
 
-  int stage = 0, piece = 0;
-  for (int64_t at = t0; at < t1; ++piece) {
+  // where the lane's operands lie in a stage: words of keys g (+ 8, + 16, ...), of values 2t (+ ...)
+  const uint32_t get_k = g * S::kRowBytes + 16 * (kChunks == 2 ? (g >> 2) & 1 : (g >> 1) & 3) + 4 * t;
+  const uint32_t get_v = 2 * t * S::kRowBytes + 16 * (kChunks == 2 ? (t >> 1) & 1 : t) + 4 * (g & 3);
+  const uint32_t pick = g < 4 ? 0x5410u : 0x7632u;   // which half of a code word the lane's four columns are in
+
+  int stage = 0;
+  for (int at = 0; at < count;) {
     // ---- one item: rows, queries ----
-    const int64_t item_end = cur.start + cur.units, end = min(t1, item_end);
-    const int h = cur.j / p.RT, rt = cur.j % p.RT;
-    const int len = cur.len;
-    const int row0 = rt * S::kRows;
+    const int item_end = cur.start + cur.units, end = min(count, item_end);
+    const int len = cur.len, h = cur.h, row0 = cur.rt * S::kRows;
     uint32_t qf[NT][S::kBlocks][4];
-    float qs[NT][S::kBlocks][2];          // of rows 2t, 2t + 1: score scale in base 2, undoing the f16 shift
-    int hi[NT][2], lo[NT][2];             // keys [lo, hi) that those rows see
-    int full_lo = 0, full_hi = 0x7FFFFFFF, seen_lo = 0x7FFFFFFF, seen_hi = 0;
+    float qs[NT][2];                      // of rows 2t, 2t + 1: score scale in base 2, undoing the f16 shift
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int r = row0 + 8 * i + g;
       const bool real = r < p.R;
       const int qi = real ? r / p.G : 0, hd = h * p.G + (real ? r % p.G : 0);
       const uint16_t* src = p.q + (static_cast<int64_t>(cur.b) * p.Lq + qi) * p.q_stride + static_cast<int64_t>(hd) * D;
+      uint4 u[S::kBlocks];
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < S::kBlocks; ++k)
+        u[k] = real ? __ldg(reinterpret_cast<const uint4*>(src + 32 * k + 8 * t)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int k = 0; k < S::kBlocks; ++k) {
-        const uint4 u = real ? __ldg(reinterpret_cast<const uint4*>(src + 32 * k + 8 * t)) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t top = 0;
+        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) top = max(top, max((w[x] << 16) & 0x7FFF0000u, w[x] & 0x7FFF0000u));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^(14 - exponent) and its inverse, both normal fp32
-        const int ex = min(max(static_cast<int>(top >> 23), 16), 254);
-        const float up = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^(14 - exponent) and its inverse, both normal fp32
+      const int ex = min(max(static_cast<int>(top >> 23), 16), 254);
+      const float up = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+      const float down = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+#pragma unroll
+      for (int k = 0; k < S::kBlocks; ++k) {
+        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
         for (int x = 0; x < 4; ++x)
           qf[i][k][x] = pack_f16(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xFFFF0000u) * up);
-        qs[i][k][0] = __shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2;
-        qs[i][k][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2;
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int rr = row0 + 8 * i + 2 * t + x;
-        hi[i][x] = rr < p.R ? len - p.Lq + rr / p.G + 1 : 0;
-        lo[i][x] = p.window > 0 ? hi[i][x] - p.window : 0;
-      }
+      qs[i][0] = __shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2;
+      qs[i][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2;
     }
-    {
-      const int q_first = row0 / p.G, q_last = min(row0 + S::kRows, p.R) - 1;
-      const int hi_first = len - p.Lq + q_first + 1, hi_last = len - p.Lq + q_last / p.G + 1;
-      full_hi = hi_first;
-      seen_hi = max(hi_last, 0);
-      full_lo = p.window > 0 ? max(0, hi_last - p.window) : 0;
-      seen_lo = p.window > 0 ? max(0, hi_first - p.window) : 0;
-    }
+    // keys that some row (seen) and that every row (full) of the tile sees
+    const int hi_first = len - p.Lq + row0 / p.G + 1;
+    const int hi_last = len - p.Lq + (min(row0 + S::kRows, p.R) - 1) / p.G + 1;
+    const int seen_lo = p.window > 0 ? max(0, hi_first - p.window) : 0, seen_hi = max(hi_last, 0);
+    const int full_lo = p.window > 0 ? max(0, hi_last - p.window) : 0, full_hi = hi_first;
+    const int key_base = (first_seen(p, len) & ~(kUnit - 1)) - kUnit * cur.start;
 
     float o[NT][S::kBlocks][2][4];
     float m[NT][2], l[NT][2];
@@ -339,77 +371,72 @@ __global__ void __launch_bounds__(kThreads, (D == 64 || NT == 1) ? 2 : 1) kv_att
 #pragma unroll
     for (int k = 0; k < S::kBlocks; ++k) E[k] = 0;
 
-    // ---- its units that fall to this warp ----
-    const int skip = static_cast<int>((at - t0) % kWarps);
-    for (int64_t u = at + (warp - skip + kWarps) % kWarps; u < end; u += kWarps) {
+    // ---- its units in this run ----
+    for (; at < end; ++at) {
       cp_async_wait<S::kStages - 2>();
       __syncwarp();
-      const int next = stage + S::kStages - 1;
-      issue(next >= S::kStages ? next - S::kStages : next);
-      const uint8_t* sk = ring + stage * S::kStageBytes;
-      const uint8_t* sv = sk + S::kKV;
-      const uint8_t* ssk = sv + S::kKV;
-      const uint8_t* ssv = ssk + S::kSc;
-      const int pages = *reinterpret_cast<const int*>(ssv + S::kSc);
-      const int key0 = cur.first + kUnit * static_cast<int>(u - cur.start);
+      const uint32_t sk = ring + stage * S::kStageBytes;
+      const uint32_t ssk = sk + 2 * S::kKV, ssv = ssk + S::kSc;
+      {
+        const int next = stage + S::kStages - 1;
+        issue(next >= S::kStages ? next - S::kStages : next);
+      }
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
+      const int pages = lds32(sk + kPages);
+      const int key0 = key_base + kUnit * at;
 
       // scores, base 2
       float s[NT][2][4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int ka = 16 * half + g, kb = ka + 8;
-        uint32_t sca, scb;
-        if constexpr (S::kBlocks == 2) {
-          sca = *reinterpret_cast<const uint16_t*>(ssk + 2 * ka);
-          scb = *reinterpret_cast<const uint16_t*>(ssk + 2 * kb);
-        } else {
-          sca = *reinterpret_cast<const uint32_t*>(ssk + 4 * ka);
-          scb = *reinterpret_cast<const uint32_t*>(ssk + 4 * kb);
-        }
+        const uint32_t sca = lds_scales<S::kBlocks>(ssk + (16 * half + g) * S::kBlocks);
+        const uint32_t scb = lds_scales<S::kBlocks>(ssk + (16 * half + g + 8) * S::kBlocks);
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k) {
-          const int swa = S::kBlocks == 2 ? k ^ ((ka >> 2) & 1) : k ^ ((ka >> 1) & 3);
-          const int swb = S::kBlocks == 2 ? k ^ ((kb >> 2) & 1) : k ^ ((kb >> 1) & 3);
           uint32_t a[4], b[4];
-          expand(*reinterpret_cast<const uint32_t*>(sk + ka * S::kRowBytes + 16 * swa + 4 * t), a);
-          expand(*reinterpret_cast<const uint32_t*>(sk + kb * S::kRowBytes + 16 * swb + 4 * t), b);
-          const float fa = scale_f32((sca >> (8 * k)) & 0xFFu), fb = scale_f32((scb >> (8 * k)) & 0xFFu);
+          expand(lds32(sk + (get_k ^ (16 * k)) + 16 * half * S::kRowBytes), a);
+          expand(lds32(sk + (get_k ^ (16 * k)) + (16 * half + 8) * S::kRowBytes), b);
+          const float fa = __uint_as_float(exponent_of(sca, k)), fb = __uint_as_float(exponent_of(scb, k));
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(c, a[0], b[0], a[1], b[1], qf[i][k][0], qf[i][k][1]);
+            float c[4];
+            mma_f16_zero(c, a[0], b[0], a[1], b[1], qf[i][k][0], qf[i][k][1]);
             mma_f16(c, a[2], b[2], a[3], b[3], qf[i][k][2], qf[i][k][3]);
             if (k == 0) {
-              s[i][half][0] = c[0] * (fa * qs[i][k][0]);
-              s[i][half][1] = c[1] * (fa * qs[i][k][1]);
-              s[i][half][2] = c[2] * (fb * qs[i][k][0]);
-              s[i][half][3] = c[3] * (fb * qs[i][k][1]);
+              s[i][half][0] = c[0] * fa;
+              s[i][half][1] = c[1] * fa;
+              s[i][half][2] = c[2] * fb;
+              s[i][half][3] = c[3] * fb;
             } else {
-              s[i][half][0] = fmaf(c[0], fa * qs[i][k][0], s[i][half][0]);
-              s[i][half][1] = fmaf(c[1], fa * qs[i][k][1], s[i][half][1]);
-              s[i][half][2] = fmaf(c[2], fb * qs[i][k][0], s[i][half][2]);
-              s[i][half][3] = fmaf(c[3], fb * qs[i][k][1], s[i][half][3]);
+              s[i][half][0] = fmaf(c[0], fa, s[i][half][0]);
+              s[i][half][1] = fmaf(c[1], fa, s[i][half][1]);
+              s[i][half][2] = fmaf(c[2], fb, s[i][half][2]);
+              s[i][half][3] = fmaf(c[3], fb, s[i][half][3]);
             }
           }
         }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[i][half][x] *= qs[i][x & 1];
       }
-      // the lane's key's value scales (0 for a key that no row sees: what lies there does not count)
-      uint32_t ev;
-      if constexpr (S::kBlocks == 2) ev = *reinterpret_cast<const uint16_t*>(ssv + 2 * lane);
-      else ev = *reinterpret_cast<const uint32_t*>(ssv + 4 * lane);
-      const bool edge = pages != 3 || key0 < full_lo || key0 + kUnit > full_hi;
-      if (edge) {
+      // the lane's key's value scales, 0 for a key that no row sees (what lies there does not count)
+      uint32_t ev = lds_scales<S::kBlocks>(ssv + lane * S::kBlocks);
+      if (pages != 3 || key0 < full_lo || key0 + kUnit > full_hi) {
         const int key = key0 + lane;
         if (key < seen_lo || key >= seen_hi || !((pages >> (lane >> 4)) & 1)) ev = 0;
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int kk = key0 + 16 * half + g + 8 * (x >> 1);
+          for (int x = 0; x < 2; ++x) {
+            const int row = row0 + 8 * i + 2 * t + x;
+            const int hi = row < p.R ? len - p.Lq + row / p.G + 1 : 0, lo = p.window > 0 ? hi - p.window : 0;
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-              if (kk < lo[i][x & 1] || kk >= hi[i][x & 1] || !((pages >> half) & 1)) s[i][half][x] = -INFINITY;
+            for (int half = 0; half < 2; ++half) {
+              const int ka = key0 + 16 * half + g;
+              if (ka < lo || ka >= hi || !((pages >> half) & 1)) s[i][half][x] = -INFINITY;
+              if (ka + 8 < lo || ka + 8 >= hi || !((pages >> half) & 1)) s[i][half][x + 2] = -INFINITY;
+            }
           }
       }
       // does a maximum grow?
@@ -466,36 +493,24 @@ __global__ void __launch_bounds__(kThreads, (D == 64 || NT == 1) ? 2 : 1) kv_att
             l[i][x] += s[i][half][x] + s[i][half][x + 2];
           }
         }
+      // the lane's key's weight factors 2^(15 + e - E) in [0, 2^15]
+      float vf[S::kBlocks];
+#pragma unroll
+      for (int k = 0; k < S::kBlocks; ++k)
+        vf[k] = __uint_as_float(static_cast<uint32_t>(
+            max(static_cast<int>(exponent_of(ev, k)) + ((142 - E[k]) << 23), 0)));
       // O^T += V^T P^T
-      const uint32_t pick = g < 4 ? 0x5410u : 0x7632u;   // which half of a code word the lane's four columns are in
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        uint32_t eva, evb;   // value scales of keys g and g + 8
-        if constexpr (S::kBlocks == 2) {
-          eva = *reinterpret_cast<const uint16_t*>(ssv + 2 * (16 * half + g));
-          evb = *reinterpret_cast<const uint16_t*>(ssv + 2 * (16 * half + g + 8));
-        } else {
-          eva = *reinterpret_cast<const uint32_t*>(ssv + 4 * (16 * half + g));
-          evb = *reinterpret_cast<const uint32_t*>(ssv + 4 * (16 * half + g + 8));
-        }
-        const int v0 = 16 * half + 2 * t;   // the lane's keys v0, v0 + 1, v0 + 8, v0 + 9
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k) {
-          // 2^(15 + e - E) in [0, 2^15]; a masked key's scale may be anything, its weight is 0
-          const int da = static_cast<int>((eva >> (8 * k)) & 0xFFu) - E[k] + 142;
-          const int db = static_cast<int>((evb >> (8 * k)) & 0xFFu) - E[k] + 142;
-          const float fa = __uint_as_float(static_cast<uint32_t>(min(max(da, 0), 142)) << 23);
-          const float fb = __uint_as_float(static_cast<uint32_t>(min(max(db, 0), 142)) << 23);
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = v0 + (x & 1) + 8 * (x >> 1);
-            const int sw = S::kBlocks == 2 ? k ^ ((key >> 2) & 1) : k ^ ((key >> 1) & 3);
-            w[x] = *reinterpret_cast<const uint32_t*>(sv + key * S::kRowBytes + 16 * sw + 4 * (g & 3));
-          }
+          const float fa = __shfl_sync(0xffffffffu, vf[k], 16 * half + g);
+          const float fb = __shfl_sync(0xffffffffu, vf[k], 16 * half + g + 8);
+          const uint32_t v0 = sk + S::kKV + (get_v ^ (16 * k)) + 16 * half * S::kRowBytes;
           // pair the keys' codes of one column in a byte: columns 0, 2 in `even`, 1, 3 in `odd`;
-          // bytes 0, 1 of keys (v0, v0 + 1), bytes 2, 3 of keys (v0 + 8, v0 + 9)
-          const uint32_t first = __byte_perm(w[0], w[2], pick), second = __byte_perm(w[1], w[3], pick);
+          // bytes 0, 1 of keys (2t, 2t + 1), bytes 2, 3 of keys (2t + 8, 2t + 9)
+          const uint32_t first = __byte_perm(lds32(v0), lds32(v0 + 8 * S::kRowBytes), pick);
+          const uint32_t second = __byte_perm(lds32(v0 + S::kRowBytes), lds32(v0 + 9 * S::kRowBytes), pick);
           const uint32_t even = (first & 0x0F0F0F0Fu) | ((second << 4) & 0xF0F0F0F0u);
           const uint32_t odd = ((first >> 4) & 0x0F0F0F0Fu) | (second & 0xF0F0F0F0u);
           uint32_t ae[4], ao[4];
@@ -513,133 +528,120 @@ __global__ void __launch_bounds__(kThreads, (D == 64 || NT == 1) ? 2 : 1) kv_att
       __syncwarp();
     }
 
-    // ---- join the warps ----
+    // ---- the item's end in this run ----
+    const bool whole = cur.start >= 0 && item_end <= count;
+    const int64_t slot = 2 * static_cast<int64_t>(run) + (cur.start > 0 ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float v = l[i][x];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        if (g == 0) s_ml[warp][8 * i + 2 * t + x] = make_float2(m[i][x], v);
-      }
-    __syncthreads();
-    const bool whole = cur.start >= t0 && item_end <= t1;
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece > 0 ? 1 : 0);
-    // the thread's output rows: (threadIdx / 32) + 8 i
-    float inv[NT];
+        float sum = l[i][x];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int r = 8 * i + 2 * t + x, row = row0 + r;
+        const int c0 = 8 * (g & 3) + 4 * (g >> 2);   // the lane's four columns of a block
+        if (row < p.R && whole) {
+          const int hd = h * p.G + row % p.G;
+          const float base = m[i][x] == -INFINITY ? 0.f : m[i][x];
+          if (p.sinks) sum += ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base);
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          uint16_t* dst = p.out + ((static_cast<int64_t>(cur.b) * p.Lq + row / p.G) * p.Hkv * p.G + hd) * D + c0;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int r = warp + 8 * i, row = row0 + r;
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r].x);
-      const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += s_ml[w][r].y * ex2(s_ml[w][r].x - base);
-      inv[i] = 1.f;
-      if (whole) {
-        if (p.sinks && row < p.R) sum += ex2(__ldg(p.sinks + h * p.G + row % p.G) * 1.44269504088896f - base);
-        inv[i] = sum > 0.f ? 1.f / sum : 0.f;
-      } else if (lane == 0) {
-        p.part_ml[slot * S::kRows + r] = make_float2(top, sum);
-      }
-    }
-    float f[NT][2];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = 8 * i + 2 * t + x;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r].x);
-        f[i][x] = top == -INFINITY ? -INFINITY : m[i][x] - top;
-      }
-#pragma unroll
-    for (int k = 0; k < S::kBlocks; ++k) {
-      float* slab = join + (k & 1) * (kWarps * S::kRows * 32);
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float mul = ex2(f[i][x] + static_cast<float>(E[k] - 142));
-          *reinterpret_cast<float4*>(slab + (warp * S::kRows + 8 * i + 2 * t + x) * 32 + 8 * (g & 3) + 4 * (g >> 2)) =
-              make_float4(o[i][k][0][x] * mul, o[i][k][0][x + 2] * mul, o[i][k][1][x] * mul, o[i][k][1][x + 2] * mul);
-        }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int r = warp + 8 * i, row = row0 + r;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += slab[(w * S::kRows + r) * 32 + lane];
-        if (!whole) {
-          p.part[(slot * S::kRows + r) * D + 32 * k + lane] = v;
+          for (int k = 0; k < S::kBlocks; ++k) {
+            const float f = ex2(static_cast<float>(E[k] - 142)) * inv;
+            *reinterpret_cast<uint2*>(dst + 32 * k) =
+                make_uint2(pack_bf16(o[i][k][0][x] * f, o[i][k][0][x + 2] * f),
+                           pack_bf16(o[i][k][1][x] * f, o[i][k][1][x + 2] * f));
+          }
         } else if (row < p.R) {
-          const int64_t tok = static_cast<int64_t>(cur.b) * p.Lq + row / p.G;
-          p.out[(tok * p.Hkv * p.G + h * p.G + row % p.G) * D + 32 * k + lane] = f32_to_bf16_bits_rn(v * inv[i]);
+          if (g == 0) p.part_ml[slot * S::kRows + r] = make_float2(m[i][x], sum);
+          float* dst = p.part + (slot * S::kRows + r) * D + c0;
+#pragma unroll
+          for (int k = 0; k < S::kBlocks; ++k) {
+            const float f = ex2(static_cast<float>(E[k] - 142));
+            *reinterpret_cast<float4*>(dst + 32 * k) =
+                make_float4(o[i][k][0][x] * f, o[i][k][0][x + 2] * f, o[i][k][1][x] * f, o[i][k][1][x + 2] * f);
+          }
         }
       }
-    }
-    // the item's first CTA says where its parts lie (slot, first and last CTA); -1: no parts
-    if (threadIdx.x == 0 && cur.start >= t0) {
-      const int64_t item = static_cast<int64_t>(cur.b) * per_seq + cur.j;
+    // the run that holds the item's first unit says where its parts lie (slot, first and last
+    // run); -1: no parts
+    if (lane == 0 && cur.start >= 0) {
+      const int64_t item = (static_cast<int64_t>(cur.b) * p.Hkv + h) * p.RT + cur.rt;
       p.desc[item] = whole ? make_int4(-1, 0, 0, 0)
-                           : make_int4(static_cast<int>(slot), static_cast<int>(blockIdx.x),
-                                       static_cast<int>((item_end - 1) / per), 0);
+                           : make_int4(static_cast<int>(slot), run, static_cast<int>((t0 + item_end - 1) / per), 0);
     }
-    at = end;
-    if (at == item_end && at < t1) cur.next(p, per_seq);
+    if (at == item_end && at < count) cur.next(p);
   }
   cp_async_wait<0>();
 }
 
-// Joins the parts of the items that several CTAs shared, in CTA order.
+// Joins the parts of the items that several runs shared, in an order that the runs fix. One
+// CTA takes `rows` rows of an item: with all of them, a warp walks the parts of a row alone;
+// with one, the warps share the parts.
 template <int D, int NT>
-__global__ void __launch_bounds__(kCombineThreads) kv_attention_join_kernel(const KvAttentionArgs p) {
+__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const KvAttentionArgs p, int rows) {
   using S = Shape<D, NT>;
+  constexpr int kCols = D / 32;   // columns of a lane
+  __shared__ float s_o[kJoinThreads / 32][D];
+  __shared__ float2 s_ml[kJoinThreads / 32];
   griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sets = S::kRows / rows;   // CTAs of an item
+  const int64_t item = blockIdx.x / sets;
+  const int4 d = p.desc[item];
+  if (d.x < 0) return;
   const int per_seq = p.Hkv * p.RT;
-  constexpr int kLanes = D / 4;                               // threads of a row, four columns each
-  constexpr int kPass = kCombineThreads / kLanes;             // rows at a time
-  const int64_t items = static_cast<int64_t>(p.B) * per_seq;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int4 d = p.desc[item];
-    if (d.x < 0) continue;
-    const int b = static_cast<int>(item / per_seq), j = static_cast<int>(item % per_seq);
-    const int h = j / p.RT, row0 = (j % p.RT) * S::kRows;
-    for (int r = threadIdx.x / kLanes; r < S::kRows; r += kPass) {
-      const int row = row0 + r, c = 4 * (threadIdx.x % kLanes);
-      if (row >= p.R) break;
-      float top = -INFINITY;
-      for (int cta = d.y; cta <= d.z; ++cta) {
-        const int64_t slot = cta == d.y ? d.x : 2 * static_cast<int64_t>(cta);
-        top = fmaxf(top, p.part_ml[slot * S::kRows + r].x);
-      }
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int cta = d.y; cta <= d.z; ++cta) {
-        const int64_t slot = cta == d.y ? d.x : 2 * static_cast<int64_t>(cta);
-        const float2 ml = p.part_ml[slot * S::kRows + r];
-        const float4 x = *reinterpret_cast<const float4*>(p.part + (slot * S::kRows + r) * D + c);
-        const float f = ex2(ml.x - base);
-        sum = fmaf(f, ml.y, sum);
-        v.x = fmaf(f, x.x, v.x);
-        v.y = fmaf(f, x.y, v.y);
-        v.z = fmaf(f, x.z, v.z);
-        v.w = fmaf(f, x.w, v.w);
-      }
-      if (p.sinks) sum += ex2(__ldg(p.sinks + h * p.G + row % p.G) * 1.44269504088896f - base);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const int64_t tok = static_cast<int64_t>(b) * p.Lq + row / p.G;
-      const uint32_t lo = f32_to_bf16_bits_rn(v.x * inv) | (static_cast<uint32_t>(f32_to_bf16_bits_rn(v.y * inv)) << 16);
-      const uint32_t hi = f32_to_bf16_bits_rn(v.z * inv) | (static_cast<uint32_t>(f32_to_bf16_bits_rn(v.w * inv)) << 16);
-      *reinterpret_cast<uint2*>(p.out + (tok * p.Hkv * p.G + h * p.G + row % p.G) * D + c) = make_uint2(lo, hi);
+  const int b = static_cast<int>(item / per_seq), j = static_cast<int>(item % per_seq);
+  const int h = j / p.RT, row0 = (j % p.RT) * S::kRows;
+  const int first_row = (blockIdx.x % sets) * rows;
+  const bool shared = rows == 1;
+  for (int r = shared ? first_row : first_row + warp; r < first_row + rows; r += kJoinThreads / 32) {
+    const int row = row0 + r;
+    if (row >= p.R) break;
+    const int lo = d.y + (shared ? warp : 0), step = shared ? kJoinThreads / 32 : 1;
+    float top = -INFINITY, sum = 0.f, v[kCols];
+    for (int run = d.y + lane; run <= d.z; run += 32) {
+      const int64_t slot = run == d.y ? d.x : 2 * static_cast<int64_t>(run);
+      top = fmaxf(top, p.part_ml[slot * S::kRows + r].x);
     }
+    top = warp_max(top);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) v[c] = 0.f;
+#pragma unroll 4
+    for (int run = lo; run <= d.z; run += step) {
+      const int64_t slot = run == d.y ? d.x : 2 * static_cast<int64_t>(run);
+      const float2 ml = p.part_ml[slot * S::kRows + r];
+      const float* src = p.part + (slot * S::kRows + r) * D + kCols * lane;
+      const float f = ex2(ml.x - base);
+      sum = fmaf(f, ml.y, sum);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) v[c] = fmaf(f, src[c], v[c]);
+    }
+    if (shared) {
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) s_o[warp][kCols * lane + c] = v[c];
+      if (lane == 0) s_ml[warp] = make_float2(0.f, sum);
+      __syncthreads();
+      if (warp > 0) return;
+      sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) v[c] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinThreads / 32; ++w) {
+        sum += s_ml[w].y;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) v[c] += s_o[w][kCols * lane + c];
+      }
+    }
+    const int hd = h * p.G + row % p.G;
+    if (p.sinks) sum += ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    uint16_t* dst = p.out + ((static_cast<int64_t>(b) * p.Lq + row / p.G) * p.Hkv * p.G + hd) * D + kCols * lane;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 2) *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16(v[c] * inv, v[c + 1] * inv);
   }
 }
 
@@ -648,13 +650,15 @@ __global__ void __launch_bounds__(kCombineThreads) kv_attention_join_kernel(cons
 namespace {
 
 int tiles_n(int R) { return R > 8 ? 2 : 1; }   // 8-row tiles of an item
+int ctas_per_sm(int D, int nt) { return D == 64 || nt == 1 ? 2 : 1; }
 
 struct Layout {
   size_t desc, ml, part, bytes;
 };
 
 Layout layout(int64_t items, int R, int D, int sms) {
-  const size_t rows = static_cast<size_t>(2) * (2 * sms) * 8 * tiles_n(R);   // two slots of every CTA
+  const int nt = tiles_n(R);
+  const size_t rows = static_cast<size_t>(2) * sms * ctas_per_sm(D, nt) * kva::kWarps * 8 * nt;   // two slots a run
   Layout l;
   l.desc = 0;
   l.ml = (items * sizeof(int4) + 255) & ~static_cast<size_t>(255);
@@ -669,20 +673,22 @@ cudaError_t launch(KvAttentionArgs p, int sms, cudaStream_t st) {
   using S = Shape<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  const int grid = sms * ((D == 64 || NT == 1) ? 2 : 1);
+  const int grid = sms * S::kCtas;
   kv_attention_kernel<D, NT><<<grid, kThreads, S::kSmem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
+  // Few items are cut into many parts each: a CTA per row, its warps over the parts.
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * p.RT;
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, 8 * sms)));
-  cfg.blockDim = dim3(kCombineThreads);
+  const int rows = items < 2 * sms ? 1 : S::kRows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items * (S::kRows / rows)));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, NT>, p);
+  return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, NT>, p, rows);
 }
 
 }  // namespace
