@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstdarg>
 #include <cstring>
+#include <cmath>
 #include <cstdlib>
 
 #include "common.cuh"
@@ -1271,7 +1272,8 @@ int mxfp4_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* k_blocks, 
   a.D = D;
   a.R = a.G * Lq;
   a.window = window;
-  a.scale_log2 = scale * 1.44269504088896f;
+  a.scale_log2 = std::fabs(scale) * 1.44269504088896f;
+  a.scale_sign = scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f;
   a.out = out;
   a.err = ws->err;
   cudaError_t e = mxmoe::launch_kv_attention(a, workspace, ws->sms, static_cast<cudaStream_t>(stream));

@@ -20,7 +20,7 @@
 // Row maxima, sums and E stay with the warp and its accumulators are rescaled only in units
 // where one of them grows.
 //
-// Work split: 32-key units of all (sequence, key/value head, row tile) items in one line; every
+// Work split: units of 64 (or 32) keys of all (sequence, key/value head, row tile) items in one line; every
 // warp of the grid takes an equal run of them whatever the sequences' lengths (the lengths are
 // on the device, so each CTA finds its warps' runs by itself) and streams it through a private
 // cp.async ring, without a barrier after the start. A warp writes the items that lie wholly in
@@ -37,19 +37,23 @@ namespace kva {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnit = 32;          // keys per unit
-constexpr int kMinUnits = 2;       // least units of a warp's run
 constexpr int kJoinThreads = 256;
+
+// A unit is 64 keys of 64 values for 8 rows, else 32 keys: what the accumulators of a
+// step leave room for in 128 registers.
+constexpr int unit_keys(int D, int nt) { return D == 64 && nt == 1 ? 64 : 32; }
 
 template <int D, int NT>
 struct Shape {
+  static constexpr int kUnit = unit_keys(D, NT);
+  static constexpr int kTiles = kUnit / 16;
   static constexpr int kRows = 8 * NT;
   static constexpr int kBlocks = D / 32;               // MXFP4 blocks of a row
   static constexpr int kRowBytes = D / 2;
   static constexpr int kKV = kUnit * kRowBytes;        // bytes of a unit's keys (or values)
   static constexpr int kSc = kUnit * kBlocks;          // their scales
   static constexpr int kStageBytes = 2 * kKV + 2 * kSc + 16;
-  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kSmem = kWarps * kStages * kStageBytes;
   static constexpr int kCtas = D == 64 || NT == 1 ? 2 : 1;   // per SM, by registers
 };
@@ -108,18 +112,13 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
+__device__ __forceinline__ uint32_t lds32(const uint8_t* at) { return *reinterpret_cast<const uint32_t*>(at); }
+__device__ __forceinline__ uint32_t lds16(const uint8_t* at) { return *reinterpret_cast<const uint16_t*>(at); }
 // the scale bytes of a key's blocks (2 or 4 of them), at `at`
 template <int kBlocks>
-__device__ __forceinline__ uint32_t lds_scales(uint32_t at) {
+__device__ __forceinline__ uint32_t lds_scales(const uint8_t* at) {
   if constexpr (kBlocks == 4) return lds32(at);
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(at) : "memory");
-  return v;
+  return lds16(at);
 }
 // byte k of a word as the exponent field of an fp32: 2^(byte - 127). Byte 0 reads as zero: its
 // block's values are below 2^-124.
@@ -143,6 +142,7 @@ __device__ __forceinline__ int first_seen(const KvAttentionArgs& p, int len) {
   return p.window > 0 ? max(0, len - p.Lq + 1 - p.window) : 0;
 }
 
+template <int kUnit>
 __device__ __forceinline__ int units_of(const KvAttentionArgs& p, int len) {
   const int first = first_seen(p, len) & ~(kUnit - 1);
   return max(1, (len - first + kUnit - 1) / kUnit);   // an empty sequence still writes its zeros
@@ -150,12 +150,15 @@ __device__ __forceinline__ int units_of(const KvAttentionArgs& p, int len) {
 
 // Position in the line of units: an item (key/value head h, row tile rt of sequence b), its
 // first unit relative to the warp's run, its units.
+template <int kUnit>
 struct Cursor {
-  int b, h, rt, len, units, start;
+  int b, h, rt, len, first, units, start;
   __device__ void load(const KvAttentionArgs& p) {
     len = seq_len(p, b);
-    units = units_of(p, len);
+    first = first_seen(p, len);
+    units = units_of<kUnit>(p, len);
   }
+  __device__ int key(int unit) const { return (first & ~(kUnit - 1)) + kUnit * (unit - start); }
   __device__ void next(const KvAttentionArgs& p) {
     start += units;
     if (++rt < p.RT) return;
@@ -177,29 +180,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
   griddep_launch_dependents();   // the joining kernel may take its places; it waits for this one's end
 
   // ---- this warp's run: units [t0, t0 + count) of n ----
-  int64_t n = 0;
-  for (int b = threadIdx.x; b < p.B; b += kThreads) n += units_of(p, seq_len(p, b));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  if (lane == 0) s_sum[warp] = n;
-  __syncthreads();
-  n = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) n += s_sum[w];
-  n *= per_seq;
-  const int64_t runs = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t per = max(static_cast<int64_t>(kMinUnits), (n + runs - 1) / runs);
   // neighbouring runs go to different SMs, so that a short line still uses all of them
   const int run = warp * gridDim.x + blockIdx.x;
-  const int64_t t0 = per * run;
-  const int count = static_cast<int>(max(static_cast<int64_t>(0), min(per, n - t0)));
-  Cursor cur;
+  int64_t per = 0, t0 = 0;
+  int count = 0;
+  Cursor<S::kUnit> cur;
   cur.b = -1;
-  {
+  // pass 0 counts the line's units, pass 1 finds the run's first; a batch of one chunk of
+  // kThreads sequences needs its prefix sums once
+  for (int pass = p.B > kThreads ? 0 : 1; pass < 2; ++pass) {
     int64_t base = 0;   // units before this chunk of sequences
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
-      const int64_t u = b < p.B ? static_cast<int64_t>(units_of(p, seq_len(p, b))) * per_seq : 0;
+      const int64_t u = b < p.B ? static_cast<int64_t>(units_of<S::kUnit>(p, seq_len(p, b))) * per_seq : 0;
       int64_t pre = u;   // inclusive over the warp
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -217,7 +210,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
       }
       s_pre[threadIdx.x] = base + pre;
       __syncthreads();
-      if (count > 0 && base <= t0 && t0 < base + all) {
+      if (pass == 0 || p.B <= kThreads) {
+        const int64_t n = base + all, runs = static_cast<int64_t>(gridDim.x) * kWarps;
+        per = max(static_cast<int64_t>(64 / S::kUnit), (n + runs - 1) / runs);   // 64 keys at least
+        t0 = per * run;
+        count = static_cast<int>(max(static_cast<int64_t>(0), min(per, n - t0)));
+      }
+      if (pass == 1 && count > 0 && base <= t0 && t0 < base + all) {
         // the first sequence of the chunk whose units end after t0
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) {
@@ -240,61 +239,73 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
   if (count == 0) return;
 
   // ---- this warp's ring of units ----
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::kStages * S::kStageBytes;
+  uint8_t* const ring = smem + warp * S::kStages * S::kStageBytes;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   constexpr int kPages = 2 * S::kKV + 2 * S::kSc;   // offset of a stage's flags: which 16 keys were loaded
   constexpr int kChunks = S::kRowBytes / 16;        // 16-byte chunks of a row, one MXFP4 block each
-  constexpr int kLoads = S::kKV / 512;              // of a unit's keys, per lane; half of them for each 16 keys
-  constexpr int kScChunks = S::kSc / 16;
+  constexpr int kLoads = S::kKV / 512 / S::kTiles;  // 16-byte loads a lane makes of 16 keys (or values)
+  constexpr int kScChunks = S::kSc / 16;            // 16-byte chunks of a unit's key (or value) scales
   // A row's chunks are permuted so that the eight rows of an operand load fall in different
   // banks; the permutation of a key repeats every 8 keys.
   const uint32_t put = (lane / kChunks) * S::kRowBytes +
                        16 * ((lane % kChunks) ^ (kChunks == 2 ? (lane >> 3) & 1 : (lane >> 3) & 3));
-  const int64_t page_rows = static_cast<int64_t>(p.Hkv) << p.page_shift;
-  const int in_page = (1 << p.page_shift) - 1;
+  const int page_rows = p.Hkv << p.page_shift, in_page = (1 << p.page_shift) - 1;
+  const bool sc_val = lane >= kScChunks;                            // the lane's chunk of scales
+  const int sc_tile = (lane % kScChunks) / (kScChunks / S::kTiles);
+  const int sc_off = 16 * (lane % (kScChunks / S::kTiles));
 
-  Cursor in = cur;           // of the next unit to load
-  int in_unit = 0, in_key = 0, pid0 = 0, pid1 = 0;
-  bool in_load0 = false, in_load1 = false;
-  // looks up the pages of unit in_unit (16 keys from each: a page holds 16 keys or more)
+  Cursor<S::kUnit> in = cur;   // of the next unit to load
+  int in_unit = 0, pid = 0;    // lane i < kTiles: the page of the unit's i-th 16 keys (a page holds 16 or more)
+  bool in_need = false;
   auto look = [&]() {
     if (in_unit >= count) return;
     if (in_unit >= in.start + in.units) in.next(p);
-    const int lo = first_seen(p, in.len);   // keys that no query sees need no page
-    in_key = (lo & ~(kUnit - 1)) + kUnit * (in_unit - in.start);
-    in_load0 = in_key < in.len && in_key + 16 > lo;
-    in_load1 = in_key + 16 < in.len && in_key + 32 > lo;
-    const int32_t* row = p.block_table + static_cast<int64_t>(in.b) * p.max_pages;
-    if (in_load0) pid0 = __ldg(row + (in_key >> p.page_shift));
-    if (in_load1) pid1 = __ldg(row + ((in_key + 16) >> p.page_shift));
-  };
-  auto load16 = [&](uint32_t dst, int pid, int key, int second) {
-    const int64_t row = pid * page_rows + ((in.h << p.page_shift) + (key & in_page));
-    const uint8_t* k = p.k_blocks + row * S::kRowBytes + 16 * lane;
-    const uint8_t* v = p.v_blocks + row * S::kRowBytes + 16 * lane;
-#pragma unroll
-    for (int i = 0; i < kLoads / 2; ++i) {
-      cp_async16(dst + put + 512 * (i + second * (kLoads / 2)), k + 512 * i);
-      cp_async16(dst + put + 512 * (i + second * (kLoads / 2)) + S::kKV, v + 512 * i);
-    }
-    // 16 keys' scales: half of the chunks of keys, half of those of values
-    if (lane < kScChunks) {
-      const bool val = lane >= kScChunks / 2;
-      const int c = lane % (kScChunks / 2);
-      cp_async16(dst + 2 * S::kKV + (val ? S::kSc : 0) + second * (S::kSc / 2) + 16 * c,
-                 (val ? p.v_scales : p.k_scales) + row * S::kBlocks + 16 * c);
-    }
+    const int key = in.key(in_unit) + 16 * lane;
+    in_need = lane < S::kTiles && key < in.len && key + 16 > in.first;   // keys that no query sees need no page
+    if (in_need) pid = __ldg(p.block_table + static_cast<int64_t>(in.b) * p.max_pages + (key >> p.page_shift));
   };
   auto issue = [&](int stage) {
     if (in_unit < count) {
-      const uint32_t dst = ring + stage * S::kStageBytes;
-      const bool ok0 = in_load0 && static_cast<uint32_t>(pid0) < static_cast<uint32_t>(p.num_pages);
-      const bool ok1 = in_load1 && static_cast<uint32_t>(pid1) < static_cast<uint32_t>(p.num_pages);
-      if (ok0) load16(dst, pid0, in_key, 0);
-      if (ok1) load16(dst, pid1, in_key + 16, 1);
-      if (lane == 0) {
-        if (ok0 != in_load0 || ok1 != in_load1) set_device_error(p.err, MXMOE_EDEVICE);   // a page outside the cache
-        asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(dst + kPages), "r"((ok0 ? 1 : 0) | (ok1 ? 2 : 0)) : "memory");
+      const uint32_t dst = ring_at + stage * S::kStageBytes;
+      const bool ok = in_need && static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.num_pages);
+      if (in_need && !ok) set_device_error(p.err, MXMOE_EDEVICE);   // a page outside the cache
+      unsigned pages = __ballot_sync(0xffffffffu, ok);
+      const int key = in.key(in_unit), head = in.h << p.page_shift;
+      if (in_page >= S::kUnit - 1) {   // one page holds the unit: its keys are one run
+        if (pages) {
+          const int page = __shfl_sync(0xffffffffu, pid, __ffs(pages) - 1);
+          const int64_t row = static_cast<int64_t>(page) * page_rows + (head + (key & in_page));
+          const int64_t off = row * S::kRowBytes + 16 * lane;
+#pragma unroll
+          for (int x = 0; x < S::kTiles * kLoads; ++x) {
+            cp_async16(dst + put + 512 * x, p.k_blocks + off + 512 * x);
+            cp_async16(dst + put + 512 * x + S::kKV, p.v_blocks + off + 512 * x);
+          }
+          if (lane < 2 * kScChunks)
+            cp_async16(dst + 2 * S::kKV + 16 * lane,
+                       (sc_val ? p.v_scales : p.k_scales) + row * S::kBlocks + 16 * (lane % kScChunks));
+          pages = (1u << S::kTiles) - 1;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < S::kTiles; ++i) {
+          const int page = __shfl_sync(0xffffffffu, pid, i);
+          if (!((pages >> i) & 1)) continue;
+          const int64_t row = static_cast<int64_t>(page) * page_rows + (head + ((key + 16 * i) & in_page));
+          const int64_t off = row * S::kRowBytes + 16 * lane;
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) {
+            cp_async16(dst + put + 512 * (i * kLoads + x), p.k_blocks + off + 512 * x);
+            cp_async16(dst + put + 512 * (i * kLoads + x) + S::kKV, p.v_blocks + off + 512 * x);
+          }
+        }
+        const int page = __shfl_sync(0xffffffffu, pid, sc_tile);
+        if (lane < 2 * kScChunks && ((pages >> sc_tile) & 1)) {
+          const int64_t row = static_cast<int64_t>(page) * page_rows + (head + ((key + 16 * sc_tile) & in_page));
+          cp_async16(dst + 2 * S::kKV + 16 * lane, (sc_val ? p.v_scales : p.k_scales) + row * S::kBlocks + sc_off);
+        }
       }
+      if (lane == 0) *reinterpret_cast<unsigned*>(ring + stage * S::kStageBytes + kPages) = pages;
       ++in_unit;
     }
     cp_async_commit();
@@ -306,8 +317,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
 
   // where the lane's operands lie in a stage: words of keys g (+ 8, + 16, ...), of values 2t (+ ...)
   const uint32_t get_k = g * S::kRowBytes + 16 * (kChunks == 2 ? (g >> 2) & 1 : (g >> 1) & 3) + 4 * t;
-  const uint32_t get_v = 2 * t * S::kRowBytes + 16 * (kChunks == 2 ? (t >> 1) & 1 : t) + 4 * (g & 3);
-  const uint32_t pick = g < 4 ? 0x5410u : 0x7632u;   // which half of a code word the lane's four columns are in
+  const uint32_t get_v = 2 * t * S::kRowBytes + 16 * (kChunks == 2 ? (t >> 1) & 1 : t) + 4 * (g & 3) + 2 * (g >> 2);
 
   int stage = 0;
   for (int at = 0; at < count;) {
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // 2^(14 - exponent) and its inverse, both normal fp32
       const int ex = min(max(static_cast<int>(top >> 23), 16), 254);
-      const float up = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+      const float up = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23) * p.scale_sign;
       const float down = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
 #pragma unroll
       for (int k = 0; k < S::kBlocks; ++k) {
@@ -346,19 +356,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
         for (int x = 0; x < 4; ++x)
           qf[i][k][x] = pack_f16(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xFFFF0000u) * up);
       }
-      qs[i][0] = __shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2;
-      qs[i][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2;
+      // never zero: a masked score's -infinity stays one under it
+      qs[i][0] = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2, 0x1p-126f);
+      qs[i][1] = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2, 0x1p-126f);
     }
     // keys that some row (seen) and that every row (full) of the tile sees
     const int hi_first = len - p.Lq + row0 / p.G + 1;
     const int hi_last = len - p.Lq + (min(row0 + S::kRows, p.R) - 1) / p.G + 1;
     const int seen_lo = p.window > 0 ? max(0, hi_first - p.window) : 0, seen_hi = max(hi_last, 0);
     const int full_lo = p.window > 0 ? max(0, hi_last - p.window) : 0, full_hi = hi_first;
-    const int key_base = (first_seen(p, len) & ~(kUnit - 1)) - kUnit * cur.start;
 
     float o[NT][S::kBlocks][2][4];
-    float m[NT][2], l[NT][2];
-    int E[S::kBlocks];
+    float m[NT][2], l[NT][2];   // m before the row's factor, so that the largest weight is exactly 1
+    float base[NT][2], vf[S::kBlocks];
+    int E[S::kBlocks];   // as an fp32's exponent field
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -366,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[i][k][0][x] = o[i][k][1][x] = 0.f;
       m[i][0] = m[i][1] = -INFINITY;
-      l[i][0] = l[i][1] = 0.f;
+      l[i][0] = l[i][1] = base[i][0] = base[i][1] = 0.f;
     }
 #pragma unroll
     for (int k = 0; k < S::kBlocks; ++k) E[k] = 0;
@@ -375,56 +386,63 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
     for (; at < end; ++at) {
       cp_async_wait<S::kStages - 2>();
       __syncwarp();
-      const uint32_t sk = ring + stage * S::kStageBytes;
-      const uint32_t ssk = sk + 2 * S::kKV, ssv = ssk + S::kSc;
+      const uint8_t* sk = ring + stage * S::kStageBytes;
+      const uint8_t *ssk = sk + 2 * S::kKV, *ssv = ssk + S::kSc;
       {
         const int next = stage + S::kStages - 1;
         issue(next >= S::kStages ? next - S::kStages : next);
       }
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
-      const int pages = lds32(sk + kPages);
-      const int key0 = key_base + kUnit * at;
+      const unsigned pages = lds32(sk + kPages);
+      const int key0 = cur.key(at);
 
-      // scores, base 2
-      float s[NT][2][4];
+      // scores, before the row's factor
+      float s[NT][S::kTiles][4];
+      float kf[S::kBlocks];   // the scales of the lane's key of 32
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t sca = lds_scales<S::kBlocks>(ssk + (16 * half + g) * S::kBlocks);
-        const uint32_t scb = lds_scales<S::kBlocks>(ssk + (16 * half + g + 8) * S::kBlocks);
+      for (int y = 0; y < S::kTiles; ++y) {
+        if (y % 2 == 0) {
+          const uint32_t sc = lds_scales<S::kBlocks>(ssk + (16 * y + lane) * S::kBlocks);
+#pragma unroll
+          for (int k = 0; k < S::kBlocks; ++k) kf[k] = __uint_as_float(exponent_of(sc, k));
+        }
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k) {
           uint32_t a[4], b[4];
-          expand(lds32(sk + (get_k ^ (16 * k)) + 16 * half * S::kRowBytes), a);
-          expand(lds32(sk + (get_k ^ (16 * k)) + (16 * half + 8) * S::kRowBytes), b);
-          const float fa = __uint_as_float(exponent_of(sca, k)), fb = __uint_as_float(exponent_of(scb, k));
+          expand(lds32(sk + (get_k ^ (16 * k)) + 16 * y * S::kRowBytes), a);
+          expand(lds32(sk + (get_k ^ (16 * k)) + (16 * y + 8) * S::kRowBytes), b);
+          const float fa = __shfl_sync(0xffffffffu, kf[k], 16 * (y % 2) + g);
+          const float fb = __shfl_sync(0xffffffffu, kf[k], 16 * (y % 2) + g + 8);
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             float c[4];
             mma_f16_zero(c, a[0], b[0], a[1], b[1], qf[i][k][0], qf[i][k][1]);
             mma_f16(c, a[2], b[2], a[3], b[3], qf[i][k][2], qf[i][k][3]);
             if (k == 0) {
-              s[i][half][0] = c[0] * fa;
-              s[i][half][1] = c[1] * fa;
-              s[i][half][2] = c[2] * fb;
-              s[i][half][3] = c[3] * fb;
+              s[i][y][0] = c[0] * fa;
+              s[i][y][1] = c[1] * fa;
+              s[i][y][2] = c[2] * fb;
+              s[i][y][3] = c[3] * fb;
             } else {
-              s[i][half][0] = fmaf(c[0], fa, s[i][half][0]);
-              s[i][half][1] = fmaf(c[1], fa, s[i][half][1]);
-              s[i][half][2] = fmaf(c[2], fb, s[i][half][2]);
-              s[i][half][3] = fmaf(c[3], fb, s[i][half][3]);
+              s[i][y][0] = fmaf(c[0], fa, s[i][y][0]);
+              s[i][y][1] = fmaf(c[1], fa, s[i][y][1]);
+              s[i][y][2] = fmaf(c[2], fb, s[i][y][2]);
+              s[i][y][3] = fmaf(c[3], fb, s[i][y][3]);
             }
           }
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) s[i][half][x] *= qs[i][x & 1];
       }
-      // the lane's key's value scales, 0 for a key that no row sees (what lies there does not count)
-      uint32_t ev = lds_scales<S::kBlocks>(ssv + lane * S::kBlocks);
-      if (pages != 3 || key0 < full_lo || key0 + kUnit > full_hi) {
-        const int key = key0 + lane;
-        if (key < seen_lo || key >= seen_hi || !((pages >> (lane >> 4)) & 1)) ev = 0;
+      // the value scales of the lane's keys (lane, lane + 32), 0 for a key that no row sees (what
+      // lies there does not count)
+      uint32_t ev[S::kUnit / 32];
+#pragma unroll
+      for (int e = 0; e < S::kUnit / 32; ++e) ev[e] = lds_scales<S::kBlocks>(ssv + (32 * e + lane) * S::kBlocks);
+      if (pages != (1u << S::kTiles) - 1 || key0 < full_lo || key0 + S::kUnit > full_hi) {
+#pragma unroll
+        for (int e = 0; e < S::kUnit / 32; ++e) {
+          const int key = key0 + 32 * e + lane;
+          if (key < seen_lo || key >= seen_hi || !((pages >> (2 * e + (lane >> 4))) & 1)) ev[e] = 0;
+        }
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -432,10 +450,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
             const int row = row0 + 8 * i + 2 * t + x;
             const int hi = row < p.R ? len - p.Lq + row / p.G + 1 : 0, lo = p.window > 0 ? hi - p.window : 0;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int ka = key0 + 16 * half + g;
-              if (ka < lo || ka >= hi || !((pages >> half) & 1)) s[i][half][x] = -INFINITY;
-              if (ka + 8 < lo || ka + 8 >= hi || !((pages >> half) & 1)) s[i][half][x + 2] = -INFINITY;
+            for (int y = 0; y < S::kTiles; ++y) {
+              const int ka = key0 + 16 * y + g;
+              const bool gone = !((pages >> y) & 1);
+              if (gone || ka < lo || ka >= hi) s[i][y][x] = -INFINITY;
+              if (gone || ka + 8 < lo || ka + 8 >= hi) s[i][y][x + 2] = -INFINITY;
             }
           }
       }
@@ -446,17 +465,25 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          mx[i][x] = fmaxf(fmaxf(s[i][0][x], s[i][0][x + 2]), fmaxf(s[i][1][x], s[i][1][x + 2]));
+          mx[i][x] = fmaxf(s[i][0][x], s[i][0][x + 2]);
+#pragma unroll
+          for (int y = 1; y < S::kTiles; ++y) mx[i][x] = fmaxf(mx[i][x], fmaxf(s[i][y][x], s[i][y][x + 2]));
           grows |= mx[i][x] > m[i][x];
         }
+      uint32_t top[S::kBlocks];
 #pragma unroll
-      for (int k = 0; k < S::kBlocks; ++k) grows |= static_cast<int>((ev >> (8 * k)) & 0xFFu) > E[k];
+      for (int k = 0; k < S::kBlocks; ++k) {
+        top[k] = 0;
+#pragma unroll
+        for (int e = 0; e < S::kUnit / 32; ++e) top[k] = max(top[k], exponent_of(ev[e], k));
+        grows |= static_cast<int>(top[k]) > E[k];
+      }
       if (__any_sync(0xffffffffu, grows)) {
-        int dE[S::kBlocks];
+        float dE[S::kBlocks];
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k) {
-          const int e = max(E[k], static_cast<int>(__reduce_max_sync(0xffffffffu, (ev >> (8 * k)) & 0xFFu)));
-          dE[k] = E[k] - e;
+          const int e = max(E[k], static_cast<int>(__reduce_max_sync(0xffffffffu, top[k])));
+          dE[k] = static_cast<float>((E[k] - e) >> 23);
           E[k] = e;
         }
 #pragma unroll
@@ -468,12 +495,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             const float nm = fmaxf(m[i][x], v);
-            const float d = nm == -INFINITY ? 0.f : m[i][x] - nm;   // nothing seen yet: all zero anyway
+            const float d = nm == -INFINITY ? 0.f : (m[i][x] - nm) * qs[i][x];   // nothing seen yet: all zero anyway
             m[i][x] = nm;
+            base[i][x] = nm == -INFINITY ? 0.f : nm;
             l[i][x] *= ex2(d);
 #pragma unroll
             for (int k = 0; k < S::kBlocks; ++k) {
-              const float f = ex2(d + static_cast<float>(dE[k]));
+              const float f = ex2(d + dE[k]);
               o[i][k][0][x] *= f;
               o[i][k][0][x + 2] *= f;
               o[i][k][1][x] *= f;
@@ -484,33 +512,31 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float base = m[i][x] == -INFINITY ? 0.f : m[i][x];
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            s[i][half][x] = ex2(s[i][half][x] - base);
-            s[i][half][x + 2] = ex2(s[i][half][x + 2] - base);
-            l[i][x] += s[i][half][x] + s[i][half][x + 2];
+          for (int y = 0; y < S::kTiles; ++y) {
+            s[i][y][x] = ex2((s[i][y][x] - base[i][x]) * qs[i][x]);
+            s[i][y][x + 2] = ex2((s[i][y][x + 2] - base[i][x]) * qs[i][x]);
+            l[i][x] += s[i][y][x] + s[i][y][x + 2];
           }
-        }
-      // the lane's key's weight factors 2^(15 + e - E) in [0, 2^15]
-      float vf[S::kBlocks];
-#pragma unroll
-      for (int k = 0; k < S::kBlocks; ++k)
-        vf[k] = __uint_as_float(static_cast<uint32_t>(
-            max(static_cast<int>(exponent_of(ev, k)) + ((142 - E[k]) << 23), 0)));
       // O^T += V^T P^T
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int y = 0; y < S::kTiles; ++y) {
+        if (y % 2 == 0) {
+          // the weight factors 2^(15 + e - E) in [0, 2^15] of the lane's key of these 32
+#pragma unroll
+          for (int k = 0; k < S::kBlocks; ++k)
+            vf[k] = __int_as_float(max(static_cast<int>(exponent_of(ev[y / 2], k)) - E[k] + (142 << 23), 0));
+        }
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k) {
-          const float fa = __shfl_sync(0xffffffffu, vf[k], 16 * half + g);
-          const float fb = __shfl_sync(0xffffffffu, vf[k], 16 * half + g + 8);
-          const uint32_t v0 = sk + S::kKV + (get_v ^ (16 * k)) + 16 * half * S::kRowBytes;
+          const float fa = __shfl_sync(0xffffffffu, vf[k], 16 * (y % 2) + g);
+          const float fb = __shfl_sync(0xffffffffu, vf[k], 16 * (y % 2) + g + 8);
+          const uint8_t* v0 = sk + S::kKV + (get_v ^ (16 * k)) + 16 * y * S::kRowBytes;
           // pair the keys' codes of one column in a byte: columns 0, 2 in `even`, 1, 3 in `odd`;
           // bytes 0, 1 of keys (2t, 2t + 1), bytes 2, 3 of keys (2t + 8, 2t + 9)
-          const uint32_t first = __byte_perm(lds32(v0), lds32(v0 + 8 * S::kRowBytes), pick);
-          const uint32_t second = __byte_perm(lds32(v0 + S::kRowBytes), lds32(v0 + 9 * S::kRowBytes), pick);
+          const uint32_t first = lds16(v0) + lds16(v0 + 8 * S::kRowBytes) * 65536u;
+          const uint32_t second = lds16(v0 + S::kRowBytes) + lds16(v0 + 9 * S::kRowBytes) * 65536u;
           const uint32_t even = (first & 0x0F0F0F0Fu) | ((second << 4) & 0xF0F0F0F0u);
           const uint32_t odd = ((first >> 4) & 0x0F0F0F0Fu) | (second & 0xF0F0F0F0u);
           uint32_t ae[4], ao[4];
@@ -518,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
           expand(odd, ao);
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            const uint32_t b0 = transpose8x8(pack_f16(s[i][half][0] * fa, s[i][half][1] * fa));
-            const uint32_t b1 = transpose8x8(pack_f16(s[i][half][2] * fb, s[i][half][3] * fb));
+            const uint32_t b0 = transpose8x8(pack_f16(s[i][y][0] * fa, s[i][y][1] * fa));
+            const uint32_t b1 = transpose8x8(pack_f16(s[i][y][2] * fb, s[i][y][3] * fb));
             mma_f16(o[i][k][0], ae[0], ao[0], ae[2], ao[2], b0, b1);
             mma_f16(o[i][k][1], ae[1], ao[1], ae[3], ao[3], b0, b1);
           }
@@ -543,23 +569,22 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
         const int c0 = 8 * (g & 3) + 4 * (g >> 2);   // the lane's four columns of a block
         if (row < p.R && whole) {
           const int hd = h * p.G + row % p.G;
-          const float base = m[i][x] == -INFINITY ? 0.f : m[i][x];
-          if (p.sinks) sum += ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base);
+          if (p.sinks) sum += ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base[i][x] * qs[i][x]);
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
           uint16_t* dst = p.out + ((static_cast<int64_t>(cur.b) * p.Lq + row / p.G) * p.Hkv * p.G + hd) * D + c0;
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k) {
-            const float f = ex2(static_cast<float>(E[k] - 142)) * inv;
+            const float f = ex2(static_cast<float>((E[k] >> 23) - 142)) * inv;
             *reinterpret_cast<uint2*>(dst + 32 * k) =
                 make_uint2(pack_bf16(o[i][k][0][x] * f, o[i][k][0][x + 2] * f),
                            pack_bf16(o[i][k][1][x] * f, o[i][k][1][x + 2] * f));
           }
         } else if (row < p.R) {
-          if (g == 0) p.part_ml[slot * S::kRows + r] = make_float2(m[i][x], sum);
+          if (g == 0) p.part_ml[slot * S::kRows + r] = make_float2(m[i][x] * qs[i][x], sum);
           float* dst = p.part + (slot * S::kRows + r) * D + c0;
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k) {
-            const float f = ex2(static_cast<float>(E[k] - 142));
+            const float f = ex2(static_cast<float>((E[k] >> 23) - 142));
             *reinterpret_cast<float4*>(dst + 32 * k) =
                 make_float4(o[i][k][0][x] * f, o[i][k][0][x + 2] * f, o[i][k][1][x] * f, o[i][k][1][x + 2] * f);
           }

@@ -245,7 +245,7 @@ struct KvAttentionArgs {
   int B, Lq, Hkv, G, D;
   int R;                        // G * Lq rows share a key/value head's keys
   int window;                   // 0: none
-  float scale_log2;             // softmax scale * log2(e)
+  float scale_log2, scale_sign; // |softmax scale| * log2(e); its sign, 0 for a scale of 0
   uint16_t* out;                // (B, Lq, Hkv * G, D)
   int* err;
   int RT;                       // row tiles of an item
