@@ -59,6 +59,10 @@ extern "C" {
 #define MXMOE_OUT_F32 0
 #define MXMOE_OUT_BF16 1
 
+#define MXMOE_ACT_NONE 0
+#define MXMOE_ACT_SILU 1         /* v * sigmoid(v) */
+#define MXMOE_ACT_GELU 2         /* v * (1 + erf(v / sqrt(2))) / 2 */
+
 /* mxfp4_quantize -- "quantization_mxfp4", Primitives (quantize_to_mxfp4).
  * w: device fp32 (rows, K). Writes blocks: device (rows, K/2) uint8 and scales: device
  * (rows, K/32) uint8. Per 32-value block: e = clamp(floor(log2(amax)) - 2, -127, 127),
@@ -282,6 +286,22 @@ int moe_mxfp4_calibrate(const uint16_t* x, const uint16_t* router_w, const uint1
 int rmsnorm_residual(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, const uint16_t* weight,
                      float eps, int T, int H, uint16_t* sum_out, uint16_t* y, uint8_t* q, float* q_scale,
                      const float* act_scale, void* stream);
+
+/* fp8_linear_fused -- the FP8 E4M3 linear of the attention projections ("gpt-oss-120b-mxfp4-
+ * fp8attn-v2", Model Details) on codes that are quantized already (rmsnorm_residual's q,
+ * moe_fp8_quantize), with finer scales and the rest of the projection in its epilogue:
+ *   out[t, n] = bf16( act( s_x[t] s_w[n] sum_k xq[t, k] wq[n, k] + bias[n] ) + residual[t, n] )
+ * all fp32 up to the one rounding. xq: device E4M3 codes (T, K); wq: device E4M3 codes (N, K);
+ * s_x: device fp32 (T), or NULL and s_x_all for all tokens; s_w: device fp32 (N), or NULL and
+ * s_w_all for all channels; bias: device fp32 (N) or NULL; act: MXMOE_ACT_NONE, _SILU or _GELU;
+ * residual: device bf16 (T, N) or NULL; out: device bf16 (T, N), which may be the residual's
+ * own memory. Errors: MXMOE_EALIGN (K % 32, N % 8), MXMOE_EUNSUPPORTED (act; a size of 2^24),
+ * MXMOE_EINVAL (sizes, a number that is no scale, null or misaligned pointers: all 16-byte
+ * aligned), MXMOE_ECUDA. One launch, no workspace: calls on several streams may overlap, and
+ * the same call gives the same bits. T = 0 is a no-op. */
+int fp8_linear_fused(const uint8_t* xq, int T, int K, const uint8_t* wq, int N, const float* s_x, float s_x_all,
+                     const float* s_w, float s_w_all, const float* bias, int act, const uint16_t* residual,
+                     uint16_t* out, void* stream);
 
 /* The paged MXFP4 key/value cache of mxfp4_kv_append and mxfp4_kv_attention ("quantization_
  * mxfp4" (KerasFormers), Primitives, along the head dimension D): k_blocks, v_blocks: device

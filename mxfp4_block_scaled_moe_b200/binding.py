@@ -42,6 +42,7 @@ _SIGS = {
     "moe_mxfp4_experts": [_vp, _vp, _i32, _i32, _i32, _i32] + [_vp] * 9,
     "moe_combine": [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp],
     "rmsnorm_residual": [_vp, _i64, _vp, _i64, _vp, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
+    "fp8_linear_fused": [_vp, _i32, _i32, _vp, _i32, _vp, _f32, _vp, _f32, _vp, _i32, _vp, _vp, _vp],
     "mxfp4_kv_append": [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _vp],
     "mxfp4_kv_attention_workspace": [_i32, _i32, _i32, _i32, _i32, _vp],
     "mxfp4_kv_attention": [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _i32, _vp, _vp] + [_i32] * 5
@@ -481,6 +482,34 @@ def rmsnorm_residual_fp8(x, weight, residual=None, eps=1e-5, act_scale=None, sum
     scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if act_scale is None else None
     _norm(x, weight, residual, eps, sum_out, y, q, scale, act_scale)
     return q, scale, sum_out
+
+
+ACTS = {None: 0, "silu": 1, "gelu": 2}
+
+
+@_on_stream
+def fp8_linear_fused(xq, wq, s_x, s_w, bias=None, act=None, residual=None, out=None):
+    """bf16 (T, N) = act(s_x s_w xq . wq^T + bias) + residual, of E4M3 codes (uint8) xq (T, K)
+    and wq (N, K). s_x: a float, or fp32 (T), one scale per token; s_w: a float, or fp32 (N),
+    one per output channel; act: None, "silu" or "gelu" (by erf); bias fp32 (N); residual
+    bf16 (T, N). out may be `residual` (the stream updated in place)."""
+    dev = _device(xq, "xq")
+    T, K = xq.shape
+    N = wq.shape[0]
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {list(ACTS)}, got {act!r}")
+    px = pw = None
+    if isinstance(s_x, torch.Tensor):
+        px, s_x = _arg(s_x, torch.float32, (T,), dev, "s_x"), 1.0
+    if isinstance(s_w, torch.Tensor):
+        pw, s_w = _arg(s_w, torch.float32, (N,), dev, "s_w"), 1.0
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=xq.device)
+    _run_on(dev, "fp8_linear_fused", _arg(xq, torch.uint8, (T, K), dev, "xq"), T, K,
+            _arg(wq, torch.uint8, (N, K), dev, "wq"), N, px, s_x, pw, s_w, _arg(bias, torch.float32, (N,), dev, "bias"),
+            ACTS[act], _arg(residual, torch.bfloat16, (T, N), dev, "residual"),
+            _arg(out, torch.bfloat16, (T, N), dev, "out"))
+    return out
 
 
 def _cache(k_blocks, k_scales, v_blocks, v_scales, dev):

@@ -1164,6 +1164,40 @@ int rmsnorm_residual(const uint16_t* x, int64_t ldx, const uint16_t* residual, i
   return MXMOE_OK;
 }
 
+int fp8_linear_fused(const uint8_t* xq, int T, int K, const uint8_t* wq, int N, const float* s_x, float s_x_all,
+                     const float* s_w, float s_w_all, const float* bias, int act, const uint16_t* residual,
+                     uint16_t* out, void* stream) {
+  t_last_error.clear();
+  t_last_launches = 0;
+  if (T < 0 || K <= 0 || N <= 0) return fail(MXMOE_EINVAL, "T = %d must be >= 0, K = %d and N = %d positive", T, K, N);
+  if (K % 32) return fail(MXMOE_EALIGN, "K = %d is not a multiple of 32", K);
+  if (N % 8) return fail(MXMOE_EALIGN, "N = %d is not a multiple of 8", N);
+  if (T >= (1 << 24) || K >= (1 << 24) || N >= (1 << 24))
+    return fail(MXMOE_EUNSUPPORTED, "T, K and N must be below 2^24");
+  if (act != MXMOE_ACT_NONE && act != MXMOE_ACT_SILU && act != MXMOE_ACT_GELU)
+    return fail(MXMOE_EUNSUPPORTED, "act = %d is none of MXMOE_ACT_NONE, _SILU, _GELU", act);
+  const float big = 3.4028234663852886e38f;
+  if ((!s_x && !(s_x_all > 0.0f && s_x_all <= big)) || (!s_w && !(s_w_all > 0.0f && s_w_all <= big)))
+    return fail(MXMOE_EINVAL, "a scale given as a number must be > 0 and finite");
+  if (T == 0) return MXMOE_OK;
+  if (!xq || !wq || !out) return fail(MXMOE_EINVAL, "null pointer");
+  const void* ptrs[] = {xq, wq, s_x, s_w, bias, residual, out};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return fail(MXMOE_EINVAL, "every pointer must be 16-byte aligned");
+  if (!mxmoe::fp8_linear_supported()) return fail(MXMOE_EUNSUPPORTED, "cuTensorMapEncodeTiled is unavailable");
+  Workspace* ws = nullptr;
+  if (int rc = current_device_ws(&ws)) return rc;
+  const mxmoe::LinearFusedArgs a{xq, wq, s_x, s_w, (s_x ? 1.0f : s_x_all) * (s_w ? 1.0f : s_w_all),
+                                 bias, residual, out, T, K, N, act, ws->err};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  StageTimer tm(st);
+  cudaError_t e = mxmoe::launch_fp8_linear_fused(a, ws->sms, st);
+  if (e) return cuda_fail(e, "fp8 linear (fused)");
+  tm.mark("fp8_gemm");
+  t_last_launches = 1;
+  return MXMOE_OK;
+}
+
 // log2 of a cache's page size, or -1 if it is none of 16, 32, 64, 128, 256
 static int page_shift_of(int page_size) {
   for (int s = 4; s <= 8; ++s)

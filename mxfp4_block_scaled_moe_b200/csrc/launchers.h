@@ -256,6 +256,21 @@ struct KvAttentionArgs {
 size_t kv_attention_workspace(int B, int Lq, int Hq, int Hkv, int D, int sms);
 cudaError_t launch_kv_attention(KvAttentionArgs a, void* workspace, int sms, cudaStream_t st);
 
+// FP8 linear on E4M3 codes with a fused epilogue (csrc/linear_fused_sm100.cu)
+struct LinearFusedArgs {
+  const uint8_t* xq;            // (T, K)
+  const uint8_t* wq;            // (N, K)
+  const float* sx;              // (T) or null
+  const float* sw;              // (N) or null
+  float s;                      // product of the scales given as numbers
+  const float* bias;            // (N) or null
+  const uint16_t* residual;     // (T, N) or null
+  uint16_t* out;                // (T, N)
+  int T, K, N, act;
+  int* err;
+};
+cudaError_t launch_fp8_linear_fused(const LinearFusedArgs& a, int sms, cudaStream_t st);
+
 // mxmoe_tc_rate_probe: back-to-back kind::mxf8f6f4 MMAs (M = 128, N = n) on `ctas` CTAs
 cudaError_t launch_tc_rate(int n, int with_copy, int random, int iters, int ctas, int* err, cudaStream_t st);
 

@@ -1,0 +1,541 @@
+// FP8 E4M3 linear on codes that are already quantized, with the whole tail of an attention
+// or MLP projection in its epilogue:
+//   out[t, n] = bf16( act( s_x[t] s_w[n] sum_k xq[t, k] wq[n, k] + bias[n] ) + residual[t, n] )
+// (s_x one scale or one per token, s_w one or one per output channel; fp32 from the
+// accumulator to the one rounding at the end). tcgen05 kind::f8f6f4, fp32 accumulators in
+// tensor memory, operands by TMA with 128-byte swizzle, 128 values of K per stage.
+//
+// Two kernels, by how many tiles there are (launch_fp8_linear_fused):
+//  - pair: a persistent CTA pair (cta_group::2) per 256 x 256 tile. Each CTA loads 128 rows of
+//    both operands, so a pair reads 512 rows for 65,536 outputs, a third less from L2 for each
+//    product than a 128 x 256 tile of a single CTA. Two accumulator slots: a tile's epilogue
+//    overlaps the next tile's products.
+//  - split: for few tokens, where the weights' bytes are the bound. Weight rows take the M side
+//    (128 a CTA), tokens the N side (16 to 128), and K is cut over a cluster of up to 8 CTAs
+//    so that every SM streams weights. The partial sums meet through distributed shared
+//    memory, added in rank order: no workspace, no second launch, the same bits each time.
+//
+// Every mbarrier wait gives up after about a second: the kernel then records MXMOE_ETIMEOUT,
+// lets copies in flight land, meets the rest of its cluster, frees its tensor memory and
+// returns.
+#include <algorithm>
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "launchers.h"
+#include "tc_common.cuh"
+#include "tmap.h"
+
+namespace mxmoe {
+namespace linf {
+
+using namespace tc;
+
+constexpr int BK = 128;
+
+// kind::f8f6f4 instruction descriptor: D = F32 (bit 4), A = B = E4M3 (format 0), both K-major,
+// N/8 at bits 17..22, M/16 at bits 24..28.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int kGroup>
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kGroup == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// ------------------------------------------------------------------- cluster -------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// the address of a shared-memory object of this CTA in the cluster's CTA `rank`
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
+}
+// mbar_wait with cluster scope: some of the barrier's arrivals come from the other CTA
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  const uint32_t addr = smem_u32(bar);
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      set_device_error(err, MXMOE_ETIMEOUT);
+      return false;
+    }
+  }
+}
+// a TMA load into this CTA's memory that completes on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+// arrive on the barrier at this offset in both CTAs of the pair once the MMAs issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .b16 m;\n mov.b16 m, 3;\n"
+      " tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// ------------------------------------------------------------------- epilogue ------
+template <int kAct>
+__device__ __forceinline__ float activate(float v) {
+  if constexpr (kAct == MXMOE_ACT_SILU) return __fdividef(v, 1.0f + __expf(-v));
+  if constexpr (kAct == MXMOE_ACT_GELU) return 0.5f * v * erfcf(-0.70710678118654752f * v);
+  return v;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Eight outputs [n, n + 8) of token t from their sums; sx: the token's scale (times s_w where
+// that is one scale for all).
+template <int kAct>
+__device__ __forceinline__ void finish8(const LinearFusedArgs& p, int64_t t, int n, const float (&acc)[8], float sx) {
+  float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (p.sw) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p.sw + n)), y = __ldg(reinterpret_cast<const float4*>(p.sw + n) + 1);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w; w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+  }
+  if (p.bias) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p.bias + n)), y = __ldg(reinterpret_cast<const float4*>(p.bias + n) + 1);
+    b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w; b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
+  }
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (p.residual) r = *reinterpret_cast<const uint4*>(p.residual + t * p.N + n);
+  const uint32_t ru[4] = {r.x, r.y, r.z, r.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo = activate<kAct>(fmaf(acc[2 * i], sx * w[2 * i], b[2 * i]));
+    float hi = activate<kAct>(fmaf(acc[2 * i + 1], sx * w[2 * i + 1], b[2 * i + 1]));
+    if (p.residual) {
+      lo += __uint_as_float(ru[i] << 16);
+      hi += __uint_as_float(ru[i] & 0xFFFF0000u);
+    }
+    o[i] = pack2(lo, hi);
+  }
+  *reinterpret_cast<uint4*>(p.out + t * p.N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ------------------------------------------------------------------------- pair ----
+namespace pair {
+constexpr int BM = 256, BN = 256;      // of the pair; each CTA loads half of either
+constexpr int kStages = 6;
+constexpr int kHalf = 128 * BK;        // 16 KB: a CTA's rows of one operand
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kSmemBytes = 1024 + kStages * 2 * kHalf + 256;
+}  // namespace pair
+
+template <int kAct>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                       const LinearFusedArgs p) {
+  using namespace pair;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + kStages * kHalf;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + kStages * kHalf);   // the leader's: both CTAs' bytes
+  uint64_t* empty = full + kStages;                                     // each CTA's
+  uint64_t* acc_full = empty + kStages;                                 // each CTA's
+  uint64_t* acc_empty = acc_full + 2;                                   // the leader's: both CTAs' epilogue warps
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(acc_empty + 2);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 2) + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_x)) : "memory");
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kEpiWarps);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tmem_holder)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  const int n_tiles = (p.N + BN - 1) / BN, units = ((p.T + BM - 1) / BM) * n_tiles, nk = (p.K + BK - 1) / BK;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer -----
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step) {
+        const int m0 = (u / n_tiles) * BM + 128 * static_cast<int>(rank), n0 = (u % n_tiles) * BN + 128 * static_cast<int>(rank);
+        for (int kt = 0; kt < nk; ++kt) {
+          if (!mbar_wait_cluster(&empty[stage], phase ^ 1, abort_flag, p.err)) { ok = false; break; }
+          const uint32_t bar = peer_addr(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kHalf);
+          tma_load_2d_pair(sA + stage * kHalf, &tmap_x, bar, kt * BK, m0);
+          tma_load_2d_pair(sB + stage * kHalf, &tmap_w, bar, kt * BK, n0);
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+      }
+      // the leader's last signals have reached this CTA's barriers before it leaves
+      for (int s = 0; s < kStages && ok; ++s) {
+        ok = mbar_wait_cluster(&empty[stage], phase ^ 1, abort_flag, p.err);
+        if (++stage == kStages) { stage = 0; phase ^= 1; }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------- MMA issuer (the leader's) ------
+    if (rank == 0) {
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      const uint32_t idesc = idesc_e4m3(BM, BN);
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step, ++it) {
+        const int ab = it & 1;
+        if (!mbar_wait_cluster(&acc_empty[ab], ((it >> 1) & 1) ^ 1, abort_flag, p.err)) break;
+        tc_fence_after();
+        const uint32_t dacc = tmem + ab * BN;
+        for (int kt = 0; kt < nk; ++kt) {
+          if (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t a0 = smem_u32(sA + stage * kHalf), b0 = smem_u32(sB + stage * kHalf);
+            const int nks = min(4, (p.K - kt * BK) / 32);   // K % 32 == 0: the last stage may hold fewer steps
+            for (int kk = 0; kk < nks; ++kk)
+              mma_f8<2>(dacc, smem_desc(a0 + 32 * kk, 16, 1024, 2), smem_desc(b0 + 32 * kk, 16, 1024, 2), idesc,
+                        (kt > 0 || kk > 0) ? 1u : 0u);
+            commit_pair(&empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        if (lane == 0) commit_pair(&acc_full[ab]);
+        __syncwarp();
+      }
+    }
+  } else {
+    // --------------------------------------------------------------- epilogue -----
+    const int q = warp & 3;              // tensor-memory lane quarter of this warp
+    const int half = (warp - 2) >> 2;    // columns [128 half, 128 half + 128)
+    int it = 0;
+    for (int u = first; u < units; u += step, ++it) {
+      const int ab = it & 1;
+      const int64_t t = static_cast<int64_t>(u / n_tiles) * BM + 128 * rank + 32 * q + lane;
+      const int n0 = (u % n_tiles) * BN;
+      const float sx = t < p.T ? (p.sx ? __ldg(p.sx + t) * p.s : p.s) : 0.f;
+      if (!mbar_wait_cluster(&acc_full[ab], (it >> 1) & 1, abort_flag, p.err)) break;
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t tbase = tmem + ab * BN + (static_cast<uint32_t>(32 * q) << 16);
+      for (int c0 = 128 * half; c0 < 128 * half + 128; c0 += 32) {
+        if (n0 + c0 >= p.N) break;
+        uint32_t v[32];
+        tc_ld_32x32b_x32(tbase + c0, v);
+        if (t < p.T) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int n = n0 + c0 + 8 * j;
+            if (n < p.N) {   // N % 8 == 0: a group of 8 columns is wholly in or out
+              float a[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) a[i] = __uint_as_float(v[8 * j + i]);
+              finish8<kAct>(p, t, n, a, sx);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_peer(peer_addr(smem_u32(&acc_empty[ab]), 0));
+    }
+  }
+
+  // --------------------------------------------------------------------- teardown ---
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {   // let copies already issued land before the CTA's shared memory goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < 200000) {
+    }
+  }
+  __syncwarp();
+  cluster_sync();      // the other CTA may still signal this one's barriers or read its operands
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512));
+  }
+}
+
+// ------------------------------------------------------------------------ split ----
+namespace split {
+constexpr int BM = 128;                // weight rows
+constexpr int kThreads = 256;
+constexpr int kMaxK = 8;               // CTAs of a cluster
+constexpr int kA = BM * BK;
+constexpr int stage_bytes(int BN) { return kA + BN * BK; }
+constexpr int stages(int BN) { return BN <= 64 ? 8 : 6; }
+constexpr int tmem_cols(int BN) { return BN < 32 ? 32 : BN; }
+constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 256; }
+}  // namespace split
+
+// Cluster of ks CTAs: weight rows [128 m, + 128), tokens [BN blockIdx.y, + BN), a K range each.
+template <int BN, int kAct>
+__global__ void __launch_bounds__(split::kThreads, 1)
+fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                        const LinearFusedArgs p, int ks) {
+  using namespace split;
+  constexpr int kStages = stages(BN), kStage = stage_bytes(BN);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
+  uint64_t* empty = full + kStages;
+  uint64_t* done = empty + kStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 1);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1) + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int m0 = (blockIdx.x / ks) * BM, t0 = blockIdx.y * BN;
+  const int nk = (p.K + BK - 1) / BK, k0 = rank * nk / ks, k1 = (rank + 1) * nk / ks;
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_x)) : "memory");
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tmem_holder)),
+                 "r"(tmem_cols(BN)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int kt = k0; kt < k1; ++kt) {
+        const int i = kt - k0, stage = i % kStages;
+        if (i >= kStages && !mbar_wait(&empty[stage], (i / kStages + 1) & 1, abort_flag, p.err)) break;
+        mbar_arrive_expect_tx(&full[stage], kStage);
+        tma_load_2d(smem + stage * kStage, &tmap_w, &full[stage], kt * BK, m0);
+        tma_load_2d(smem + stage * kStage + kA, &tmap_x, &full[stage], kt * BK, t0);
+      }
+    }
+  } else if (warp == 1) {
+    bool ok = true;
+    for (int kt = k0; kt < k1; ++kt) {
+      const int i = kt - k0, stage = i % kStages;
+      if (!mbar_wait(&full[stage], (i / kStages) & 1, abort_flag, p.err)) { ok = false; break; }
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t a0 = smem_u32(smem + stage * kStage), b0 = a0 + kA;
+        const int nks = min(4, (p.K - kt * BK) / 32);
+        for (int kk = 0; kk < nks; ++kk)
+          mma_f8<1>(tmem, smem_desc(a0 + 32 * kk, 16, 1024, 2), smem_desc(b0 + 32 * kk, 16, 1024, 2),
+                    idesc_e4m3(BM, BN), (i > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(&empty[stage]);
+      }
+      __syncwarp();
+    }
+    if (ok && lane == 0) tc_commit(done);
+    __syncwarp();
+  }
+  // every stage has been consumed when `done` completes: its memory takes the partial sums,
+  // fp32 [token][128 weight rows]
+  float* sums = reinterpret_cast<float*>(smem);
+  if (warp >= 4 && mbar_wait(done, 0, abort_flag, p.err)) {
+    __syncwarp();
+    tc_fence_after();
+    const int q = warp & 3;
+    for (int c0 = 0; c0 < BN && t0 + c0 < p.T; c0 += 8) {
+      uint32_t v[8];
+      tc_ld_32x32b_x8(tmem + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
+      tc_wait_ld(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sums[(c0 + i) * BM + 32 * q + lane] = __uint_as_float(v[i]);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (*abort_flag) {   // let copies already issued land before the CTA's shared memory goes
+    const long long c0 = clock64();
+    while (clock64() - c0 < 200000) {
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+  // the cluster's CTAs share the tile's (token, 8 rows) groups; sums in rank order
+  const int tokens = min(BN, p.T - t0), groups = tokens * (BM / 8);
+  const uint32_t base = smem_u32(sums);
+  for (int gi = rank * kThreads + threadIdx.x; gi < groups; gi += ks * kThreads) {
+    const int tok = gi / (BM / 8), n = m0 + 8 * (gi % (BM / 8));
+    if (n >= p.N) continue;
+    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < ks; ++r) {
+      const uint32_t at = peer_addr(base + 4 * (tok * BM + 8 * (gi % (BM / 8))), r);
+      const float4 x = ld_peer(at), y = ld_peer(at + 16);
+      a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+      a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+    }
+    const int64_t t = t0 + tok;
+    finish8<kAct>(p, t, n, a, p.sx ? __ldg(p.sx + t) * p.s : p.s);
+  }
+  __syncwarp();
+  cluster_sync();      // this CTA's sums have been read
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(tmem_cols(BN)));
+  }
+}
+
+}  // namespace linf
+
+namespace {
+
+// (rows, K) bytes, K-major, box (BK, box_rows), 128-byte swizzle, zero fill outside
+bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t K, uint32_t box_rows) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(K)};
+  const uint32_t box[2] = {static_cast<uint32_t>(linf::BK), box_rows};
+  return tmap_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box);
+}
+
+template <int kAct>
+cudaError_t launch_pair(const LinearFusedArgs& p, int sms, cudaStream_t st) {
+  using namespace linf;
+  CUtensorMap mx, mw;
+  if (!encode_codes(&mx, p.xq, p.T, p.K, 128) || !encode_codes(&mw, p.wq, p.N, p.K, 128)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(fp8_linear_pair_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       pair::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t units = cdiv(p.T, pair::BM) * cdiv(p.N, pair::BN);
+  const int grid = 2 * static_cast<int>(std::min<int64_t>(units, sms / 2));
+  fp8_linear_pair_kernel<kAct><<<grid, pair::kThreads, pair::kSmemBytes, st>>>(mx, mw, p);
+  return cudaGetLastError();
+}
+
+template <int BN, int kAct>
+cudaError_t launch_split(const LinearFusedArgs& p, int sms, cudaStream_t st) {
+  using namespace linf;
+  CUtensorMap mx, mw;
+  if (!encode_codes(&mx, p.xq, p.T, p.K, BN) || !encode_codes(&mw, p.wq, p.N, p.K, split::BM)) return cudaErrorInvalidValue;
+  constexpr int smem = split::smem_bytes(BN);
+  cudaError_t e = cudaFuncSetAttribute(fp8_linear_split_kernel<BN, kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int m_tiles = static_cast<int>(cdiv(p.N, split::BM)), t_tiles = static_cast<int>(cdiv(p.T, BN));
+  const int nk = static_cast<int>(cdiv(p.K, BK));
+  const int ks = std::max(1, std::min({split::kMaxK, nk, sms / (m_tiles * t_tiles)}));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(m_tiles * ks), static_cast<unsigned>(t_tiles));
+  cfg.blockDim = dim3(split::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fp8_linear_split_kernel<BN, kAct>, mw, mx, p, ks);
+}
+
+template <int kAct>
+cudaError_t launch_act(const LinearFusedArgs& p, int sms, cudaStream_t st) {
+  using namespace linf;
+  const int64_t pairs = cdiv(p.T, pair::BM) * cdiv(p.N, pair::BN);
+  if (p.T > 128 && 3 * pairs >= sms) return launch_pair<kAct>(p, sms, st);
+  if (p.T <= 16) return launch_split<16, kAct>(p, sms, st);
+  if (p.T <= 32) return launch_split<32, kAct>(p, sms, st);
+  if (p.T <= 64) return launch_split<64, kAct>(p, sms, st);
+  return launch_split<128, kAct>(p, sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_linear_fused(const LinearFusedArgs& p, int sms, cudaStream_t st) {
+  if (p.act == MXMOE_ACT_SILU) return launch_act<MXMOE_ACT_SILU>(p, sms, st);
+  if (p.act == MXMOE_ACT_GELU) return launch_act<MXMOE_ACT_GELU>(p, sms, st);
+  return launch_act<MXMOE_ACT_NONE>(p, sms, st);
+}
+
+}  // namespace mxmoe

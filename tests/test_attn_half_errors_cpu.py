@@ -96,3 +96,21 @@ def test_kv_attention_argument_checks(L):
     n = ctypes.c_int64(0)
     assert L.mxfp4_kv_attention_workspace(2, 1, 8, 2, 96, ctypes.byref(n)) == EUNSUPPORTED
     assert L.mxfp4_kv_attention_workspace(2, 1, 8, 2, 64, None) == EINVAL
+
+
+def _linear(L, xq=A, T=4, K=64, wq=A, N=16, sx=None, sxa=1.0, sw=None, swa=1.0, bias=None, act=0, res=None, out=A):
+    return L.fp8_linear_fused(xq, T, K, wq, N, sx, sxa, sw, swa, bias, act, res, out, None)
+
+
+def test_linear_fused_argument_checks(L):
+    assert _linear(L, T=0) == OK and _linear(L, T=0, xq=None, out=None) == OK
+    assert _linear(L, T=-1) == EINVAL and _linear(L, K=0) == EINVAL and _linear(L, N=0) == EINVAL
+    assert _linear(L, K=48) == EALIGN and "multiple of 32" in err(L)
+    assert _linear(L, N=12) == EALIGN and "multiple of 8" in err(L)
+    assert _linear(L, T=1 << 24) == EUNSUPPORTED and _linear(L, act=3) == EUNSUPPORTED and _linear(L, act=-1) == EUNSUPPORTED
+    for s in (0.0, -1.0, float("nan"), float("inf")):
+        assert _linear(L, sxa=s) == EINVAL and _linear(L, swa=s) == EINVAL
+    for n in ("xq", "wq", "out"):
+        assert _linear(L, **{n: None}) == EINVAL
+    for n in ("xq", "wq", "out", "sx", "sw", "bias", "res"):
+        assert _linear(L, **{n: MIS}) == EINVAL and "aligned" in err(L)

@@ -1,0 +1,143 @@
+"""fp8_linear_fused against the formula in 64 bits.
+
+Bar. Products of two E4M3 values are exact in fp32; a sum of K of them is taken in K / 32
+steps, each with an error below 2^-22 of A = s_x s_w sum |xq wq| (alignment and rounding of a
+step, of the partials' joining, and of the scale products: 8 more). SiLU and GELU have slopes
+below 1.13 and an error of a few fp32 roundings of their value. Then one bf16 rounding, 2^-8.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mxfp4_block_scaled_moe_b200 import binding
+    return binding
+
+
+def _codes(g, rows, cols):
+    """E4M3 codes of normal values with the largest near 448."""
+    v = torch.randn(rows, cols, generator=g, device="cuda") * 110
+    return v.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+class Case:
+    def __init__(self, T, K, N, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed + T + K + N)
+        self.xq, self.wq = _codes(g, T, K), _codes(g, N, K)
+        self.sx = 0.01 * (0.5 + torch.rand(T, generator=g, device="cuda")) / math.sqrt(K)
+        self.sw = 0.01 * (0.5 + torch.rand(N, generator=g, device="cuda"))
+        self.bias = torch.randn(N, generator=g, device="cuda")
+        self.res = torch.randn(T, N, generator=g, device="cuda").bfloat16()
+
+    def check(self, out, s_x, s_w, bias=None, act=None, residual=None):
+        x, w = (t.view(torch.float8_e4m3fn).double() for t in (self.xq, self.wq))
+        s = torch.as_tensor(s_x, device="cuda").double().reshape(-1, 1) * torch.as_tensor(s_w, device="cuda").double()
+        y, mag = (x @ w.t()) * s, (x.abs() @ w.abs().t()) * s
+        if bias is not None:
+            y = y + bias.double()
+            mag = mag + bias.double().abs()
+        if act == "silu":
+            y = y * torch.sigmoid(y)
+        elif act == "gelu":
+            y = 0.5 * y * torch.special.erfc(-y / math.sqrt(2))
+        if residual is not None:
+            y = y + residual.double()
+            mag = mag + residual.double().abs()
+        tol = y.abs() * 2.0 ** -8 + 1.13 * mag * (x.shape[1] / 32 + 8) * 2.0 ** -22
+        assert out.dtype == torch.bfloat16 and out.shape == y.shape
+        err = (out.double() - y).abs()
+        assert bool((err <= tol).all()), (float((err - tol).max()), float(y.abs().max()))
+
+
+SHAPES = [(1, 32, 8), (1, 2880, 5120), (3, 96, 136), (16, 4096, 2880), (17, 256, 64), (32, 160, 1000), (33, 1024, 256),
+          (64, 4096, 2880), (65, 512, 384), (128, 2880, 640), (129, 128, 128), (200, 2880, 5120), (777, 1024, 4096),
+          (1000, 352, 2048), (513, 64, 8200), (3000, 288, 1544), (4100, 2880, 264), (300, 8192, 4096)]
+
+
+@pytest.mark.parametrize("T,K,N", SHAPES)
+def test_linear_fused(B, T, K, N):
+    c = Case(T, K, N)
+    sx, sw = float(c.sx[0]), float(c.sw[0])
+    kw = [dict(s_x=c.sx, s_w=c.sw, bias=c.bias, residual=c.res), dict(s_x=sx, s_w=sw),
+          dict(s_x=c.sx, s_w=sw, act="silu", bias=c.bias), dict(s_x=sx, s_w=c.sw, act="gelu", residual=c.res)]
+    for k in kw:
+        out = B.fp8_linear_fused(c.xq, c.wq, **k)
+        B.mxmoe_check()
+        c.check(out, **k)
+        assert torch.equal(B.fp8_linear_fused(c.xq, c.wq, **k), out)
+
+
+@pytest.mark.parametrize("T", [5, 600])
+def test_in_place_residual_and_given_output(B, T):
+    c = Case(T, 512, 4096)
+    want = B.fp8_linear_fused(c.xq, c.wq, c.sx, c.sw, c.bias, residual=c.res)
+    out = torch.full_like(want, float("nan"))
+    assert B.fp8_linear_fused(c.xq, c.wq, c.sx, c.sw, c.bias, residual=c.res, out=out) is out
+    assert torch.equal(out, want)
+    B.fp8_linear_fused(c.xq, c.wq, c.sx, c.sw, c.bias, residual=c.res, out=c.res)
+    assert torch.equal(c.res, want)
+
+
+@pytest.mark.parametrize("T,N", [(9, 264), (515, 4104)])
+def test_nothing_beside_the_output_is_written(B, T, N):
+    c = Case(T, 256, N)
+    guard = torch.full((T + 16, N), 7.0, device="cuda", dtype=torch.bfloat16)
+    B.fp8_linear_fused(c.xq, c.wq, c.sx, c.sw, out=guard[8:8 + T])
+    B.mxmoe_check()
+    assert bool((guard[:8] == 7).all()) and bool((guard[8 + T:] == 7).all())
+    c.check(guard[8:8 + T], c.sx, c.sw)
+
+
+def test_activation_tails(B):
+    """Pre-activations from -30 to 30: the tails keep their relative precision."""
+    xq = torch.full((1, 32), 0, dtype=torch.uint8, device="cuda")
+    wq = torch.zeros(1024, 32, dtype=torch.uint8, device="cuda")
+    bias = torch.linspace(-30, 30, 1024, device="cuda")
+    for act, f in (("silu", lambda v: v * torch.sigmoid(v)), ("gelu", lambda v: 0.5 * v * torch.special.erfc(-v / math.sqrt(2)))):
+        out = B.fp8_linear_fused(xq, wq, 1.0, 1.0, bias=bias, act=act).double()[0]
+        ref = f(bias.double())
+        # erfc's argument carries two fp32 roundings: 2 v^2 2^-24 of its value at the tail
+        assert bool(((out - ref).abs() <= ref.abs() * (2.0 ** -8 + bias.double() ** 2 * 2.0 ** -20) + 2.0 ** -126).all())
+
+
+def test_streams_and_graph(B):
+    for T in (4, 700):
+        c = Case(T, 2880, 4096)
+        want = B.fp8_linear_fused(c.xq, c.wq, c.sx, c.sw, c.bias)
+        s = [torch.cuda.Stream(), torch.cuda.Stream()]
+        torch.cuda.synchronize()
+        got = [B.fp8_linear_fused(c.xq, c.wq, c.sx, c.sw, c.bias, stream=s[i % 2]) for i in range(8)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in got)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = B.fp8_linear_fused(c.xq, c.wq, c.sx, c.sw, c.bias)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    B.mxmoe_check()
+
+
+def test_refusals(B):
+    c = Case(4, 64, 32)
+    for bad in (lambda: B.fp8_linear_fused(c.xq.float(), c.wq, 1.0, 1.0), lambda: B.fp8_linear_fused(c.xq, c.wq[:, :32], 1.0, 1.0),
+                lambda: B.fp8_linear_fused(c.xq, c.wq, c.sx[:3], 1.0), lambda: B.fp8_linear_fused(c.xq, c.wq, 1.0, c.sw.double()),
+                lambda: B.fp8_linear_fused(c.xq, c.wq, 1.0, 1.0, act="relu"),
+                lambda: B.fp8_linear_fused(c.xq, c.wq, 1.0, 1.0, residual=c.res[:, :16]),
+                lambda: B.fp8_linear_fused(c.xq, c.wq, 1.0, 1.0, bias=c.bias.cpu()),
+                lambda: B.fp8_linear_fused(c.xq.t(), c.wq, 1.0, 1.0)):
+        with pytest.raises(ValueError):
+            bad()
+    for rc, bad in ((B.EINVAL, lambda: B.fp8_linear_fused(c.xq, c.wq, 0.0, 1.0)),
+                    (B.EALIGN, lambda: B.fp8_linear_fused(c.xq[:, :48].contiguous(), c.wq[:, :48].contiguous(), 1.0, 1.0)),
+                    (B.EALIGN, lambda: B.fp8_linear_fused(c.xq, c.wq[:12], 1.0, 1.0))):
+        with pytest.raises(B.MxmoeError) as ei:
+            bad()
+        assert ei.value.rc == rc
+    assert B.fp8_linear_fused(c.xq[:0], c.wq, 1.0, 1.0).shape == (0, 32)
