@@ -8,7 +8,6 @@ bf16 tensors are passed as their bit patterns (torch.bfloat16 storage).
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -93,12 +92,13 @@ def _call(name, *args):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dev(t, dtype, name):
@@ -363,8 +363,9 @@ def moe_combine(y, topk_idx, topk_w, inv, out=None, stream=None):
 
 # -------------------------------------------------------------- attention half -----
 
-# The checks below run on every call of operators whose kernels take a few microseconds, so
-# they are flat: one helper call per tensor, the message formed only on failure.
+# These operators take a few microseconds on the GPU, so their host side is kept short: flat
+# checks whose messages are formed only on failure, no checks of tensors made here, raw
+# device and stream handles.
 
 def _device(t, name):
     dev = t.get_device()
@@ -394,10 +395,6 @@ def _arg(t, dtype, shape, dev, name):
     return t.data_ptr()
 
 
-def _dense_like(t, dtype):
-    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
-
-
 def _rows(t, H, dev, name):
     """(device pointer, row stride) of a bf16 tensor (..., H) as rows: a dense tensor of any
     rank, or two-dimensional rows cut from wider ones."""
@@ -411,8 +408,10 @@ def _rows(t, H, dev, name):
 
 
 def _run_on(dev, name, *args):
-    """_call with the tensors' device current; that device's current stream goes last."""
-    if dev != torch.cuda.current_device():
+    """_call with the tensors' device current; that device's current stream goes last. (An
+    operator given `stream` calls itself with that stream current first, so that the
+    outputs and workspaces it makes belong to the stream that uses them.)"""
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _run_on(dev, name, *args)
     L = _lib or lib()
@@ -421,78 +420,79 @@ def _run_on(dev, name, *args):
         raise MxmoeError(rc, name, L.mxmoe_last_error().decode(errors="replace"))
 
 
-def _on_stream(fn):
-    """Gives an operator its `stream` keyword: the call runs with that stream current, so
-    that the outputs and workspaces it makes belong to the stream that uses them."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
-
-
-def _norm(x, weight, residual, eps, sum_out, y, q, q_scale, act_scale):
+def _norm(x, weight, residual, eps, sum_out, y, q, fp8, act_scale):
+    """Shared by the two norms: makes the outputs that were not given, checks the rest."""
     dev = _device(x, "x")
     shape = x.shape
     H = shape[-1]
     px, ldx = _rows(x, H, dev, "x")
-    pr, ldr = None, H
+    pr = ps = py = pq = pt = s = scale = None
+    ldr = H
     if residual is not None:
         if residual.shape != shape:
             raise ValueError(f"residual must have x's shape {tuple(shape)}, got {tuple(residual.shape)}")
         pr, ldr = _rows(residual, H, dev, "residual")
-    s = None if act_scale is None else ctypes.byref(ctypes.c_float(act_scale))
+        if sum_out is None:
+            sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+            ps = sum_out.data_ptr()
+        else:
+            ps = _arg(sum_out, torch.bfloat16, shape, dev, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out goes with a residual")
+    if y is not None:
+        py = _arg(y, torch.bfloat16, shape, dev, "y")
+    elif not fp8:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        py = y.data_ptr()
+    if fp8:
+        if q is None:
+            q = torch.empty_like(x, dtype=torch.uint8, memory_format=torch.contiguous_format)
+            pq = q.data_ptr()
+        else:
+            pq = _arg(q, torch.uint8, shape, dev, "q")
+        if act_scale is None:
+            scale = x.new_empty(shape[:-1], dtype=torch.float32)
+            pt = scale.data_ptr()
+        else:
+            s = ctypes.byref(_f32(act_scale))
     _run_on(dev, "rmsnorm_residual", px, ldx, pr, ldr, _arg(weight, torch.bfloat16, (H,), dev, "weight"), eps,
-            x.numel() // H if H else 0, H, _arg(sum_out, torch.bfloat16, shape, dev, "sum_out"),
-            _arg(y, torch.bfloat16, shape, dev, "y"), _arg(q, torch.uint8, shape, dev, "q"),
-            None if q_scale is None else q_scale.data_ptr(), s)
+            x.numel() // H if H else 0, H, ps, py, pq, pt, s)
+    return y, q, scale, sum_out
 
 
-def _sum_out(x, residual, sum_out):
-    if residual is None:
-        if sum_out is not None:
-            raise ValueError("sum_out goes with a residual")
-    elif sum_out is None:
-        return _dense_like(x, torch.bfloat16)
-    return sum_out
-
-
-@_on_stream
-def rmsnorm_residual(x, weight, residual=None, eps=1e-5, sum_out=None, y=None):
+def rmsnorm_residual(x, weight, residual=None, eps=1e-5, sum_out=None, y=None, stream=None):
     """(y, sum): h = bf16(x + residual) (x without one; sum is then None) and y = bf16(h *
     weight / sqrt(mean(h^2) + eps)) over the last axis. sum_out may be `residual` (the
     stream updated in place). Strided rows of a 2-D x or residual are taken as they are."""
-    sum_out = _sum_out(x, residual, sum_out)
-    if y is None:
-        y = _dense_like(x, torch.bfloat16)
-    _norm(x, weight, residual, eps, sum_out, y, None, None, None)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rmsnorm_residual(x, weight, residual, eps, sum_out, y)
+    y, _, _, sum_out = _norm(x, weight, residual, eps, sum_out, y, None, False, None)
     return y, sum_out
 
 
-@_on_stream
-def rmsnorm_residual_fp8(x, weight, residual=None, eps=1e-5, act_scale=None, sum_out=None, q=None, y=None):
+def rmsnorm_residual_fp8(x, weight, residual=None, eps=1e-5, act_scale=None, sum_out=None, q=None, y=None,
+                         stream=None):
     """(q, scale, sum): as rmsnorm_residual with E4M3 codes (uint8) of the norm: divided by the
     static act_scale (scale is then None), or by one scale per token, max|n| / 448 (scale:
     fp32 of x's leading shape). y, if given, receives the bf16 norm too."""
-    sum_out = _sum_out(x, residual, sum_out)
-    if q is None:
-        q = _dense_like(x, torch.uint8)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if act_scale is None else None
-    _norm(x, weight, residual, eps, sum_out, y, q, scale, act_scale)
-    return q, scale, sum_out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rmsnorm_residual_fp8(x, weight, residual, eps, act_scale, sum_out, q, y)
+    return _norm(x, weight, residual, eps, sum_out, y, q, True, act_scale)[1:]
 
 
 ACTS = {None: 0, "silu": 1, "gelu": 2}
 
 
-@_on_stream
-def fp8_linear_fused(xq, wq, s_x, s_w, bias=None, act=None, residual=None, out=None):
+def fp8_linear_fused(xq, wq, s_x, s_w, bias=None, act=None, residual=None, out=None, stream=None):
     """bf16 (T, N) = act(s_x s_w xq . wq^T + bias) + residual, of E4M3 codes (uint8) xq (T, K)
     and wq (N, K). s_x: a float, or fp32 (T), one scale per token; s_w: a float, or fp32 (N),
     one per output channel; act: None, "silu" or "gelu" (by erf); bias fp32 (N); residual
     bf16 (T, N). out may be `residual` (the stream updated in place)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_linear_fused(xq, wq, s_x, s_w, bias, act, residual, out)
     dev = _device(xq, "xq")
     T, K = xq.shape
     N = wq.shape[0]
@@ -505,10 +505,12 @@ def fp8_linear_fused(xq, wq, s_x, s_w, bias=None, act=None, residual=None, out=N
         pw, s_w = _arg(s_w, torch.float32, (N,), dev, "s_w"), 1.0
     if out is None:
         out = torch.empty((T, N), dtype=torch.bfloat16, device=xq.device)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, torch.bfloat16, (T, N), dev, "out")
     _run_on(dev, "fp8_linear_fused", _arg(xq, torch.uint8, (T, K), dev, "xq"), T, K,
             _arg(wq, torch.uint8, (N, K), dev, "wq"), N, px, s_x, pw, s_w, _arg(bias, torch.float32, (N,), dev, "bias"),
-            ACTS[act], _arg(residual, torch.bfloat16, (T, N), dev, "residual"),
-            _arg(out, torch.bfloat16, (T, N), dev, "out"))
+            ACTS[act], _arg(residual, torch.bfloat16, (T, N), dev, "residual"), po)
     return out
 
 
@@ -517,10 +519,11 @@ def _cache(k_blocks, k_scales, v_blocks, v_scales, dev):
     shape = k_blocks.shape
     if len(shape) != 4:
         raise ValueError(f"k_blocks must be (num_pages, Hkv, page_size, D/2), got {tuple(shape)}")
-    sc = shape[:3] + (shape[3] // 16,)
+    pages, Hkv, page_size, half = shape
+    sc = (pages, Hkv, page_size, half // 16)
     ptrs = (_arg(k_blocks, torch.uint8, shape, dev, "k_blocks"), _arg(k_scales, torch.uint8, sc, dev, "k_scales"),
             _arg(v_blocks, torch.uint8, shape, dev, "v_blocks"), _arg(v_scales, torch.uint8, sc, dev, "v_scales"))
-    return ptrs, shape[0], shape[1], shape[2], 2 * shape[3]
+    return ptrs, pages, Hkv, page_size, 2 * half
 
 
 def _tokens(t, dev, name):
@@ -528,11 +531,14 @@ def _tokens(t, dev, name):
     whose tokens are one stride apart."""
     if t.dtype is not torch.bfloat16 or t.get_device() != dev:
         _refuse(t, torch.bfloat16, None, dev, name)
+    shape = t.shape
     if t.is_contiguous():
-        return t.data_ptr(), t.shape[-2] * t.shape[-1]
-    stride, shape = t.stride(), t.shape
+        return t.data_ptr(), shape[-2] * shape[-1]
+    stride = t.stride()
     if stride[-1] != 1 or stride[-2] != shape[-1]:
         raise ValueError(f"{name}: each token's heads must be dense")
+    if len(shape) == 3 and shape[0] > 1:
+        return t.data_ptr(), stride[0]
     step = n = None
     for size, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
         if size == 1:
@@ -546,12 +552,14 @@ def _tokens(t, dev, name):
     return t.data_ptr(), shape[-2] * shape[-1] if step is None else step
 
 
-@_on_stream
-def mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales):
+def mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales, stream=None):
     """Quantize the rows of k and v, bf16 (T, Hkv, D), to MXFP4 along D and write them to the
     paged cache: blocks (num_pages, Hkv, page_size, D/2) and scales (num_pages, Hkv, page_size,
     D/32), uint8. slots: int64 (T), page * page_size + offset; negative skips the token. k and
     v may be slices of a fused projection's rows."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales)
     dev = _device(k, "k")
     ptrs, pages, Hkv, page_size, D = _cache(k_blocks, k_scales, v_blocks, v_scales, dev)
     T = k.shape[0]
@@ -579,15 +587,18 @@ def mxfp4_kv_attention_workspace(B, Lq, Hq, Hkv, D, device=None) -> int:
     return _attention_bytes[key]
 
 
-@_on_stream
 def mxfp4_kv_attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, seq_lens, scale=None, window=0, sinks=None,
-                       out=None, workspace=None):
+                       out=None, workspace=None, stream=None):
     """Attention of q, bf16 (B, Lq, Hq, D) or (B, Hq, D), the last Lq tokens of B sequences, over
     the paged MXFP4 cache; returns bf16 of q's shape. block_table: int32 (B, max_pages);
     seq_lens: int32 (B), the new tokens included; scale: 1 / sqrt(D) unless given; window: the
     keys a query sees, itself included (0: all); sinks: fp32 (Hq) logits joining each softmax.
     q's tokens may be slices of a fused projection's rows. workspace: uint8 of at least
     mxfp4_kv_attention_workspace's size, made by the call unless given."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mxfp4_kv_attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, seq_lens, scale, window,
+                                      sinks, out, workspace)
     dev = _device(q, "q")
     ptrs, pages, Hkv, page_size, D = _cache(k_blocks, k_scales, v_blocks, v_scales, dev)
     shape = q.shape
@@ -600,16 +611,22 @@ def mxfp4_kv_attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, s
         raise ValueError(f"block_table must be (B, max_pages), got {tuple(block_table.shape)}")
     max_pages = block_table.shape[1]
     if out is None:
-        out = _dense_like(q, torch.bfloat16)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, torch.bfloat16, shape, dev, "out")
     if workspace is None:
-        key = (dev, B, Lq, Hq, Hkv, D)
-        n = _attention_bytes.get(key) or mxfp4_kv_attention_workspace(B, Lq, Hq, Hkv, D, q.device)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        nbytes = _attention_bytes.get((dev, B, Lq, Hq, Hkv, D))
+        if nbytes is None:
+            nbytes = mxfp4_kv_attention_workspace(B, Lq, Hq, Hkv, D, q.device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        pw = workspace.data_ptr()
+    else:
+        nbytes, pw = workspace.numel(), _arg(workspace, torch.uint8, workspace.shape, dev, "workspace")
     _run_on(dev, "mxfp4_kv_attention", pq, ldq, *ptrs, pages, page_size,
             _arg(block_table, torch.int32, (B, max_pages), dev, "block_table"), max_pages,
             _arg(seq_lens, torch.int32, (B,), dev, "seq_lens"), _arg(sinks, torch.float32, (Hq,), dev, "sinks"), B, Lq,
-            Hq, Hkv, D, D ** -0.5 if scale is None else scale, window, _arg(out, torch.bfloat16, shape, dev, "out"),
-            _arg(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel())
+            Hq, Hkv, D, D ** -0.5 if scale is None else scale, window, po, pw, nbytes)
     return out
 
 
