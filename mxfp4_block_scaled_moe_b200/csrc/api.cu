@@ -1273,6 +1273,10 @@ int mxfp4_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* k_blocks, 
   if (window > (1 << 30)) return fail(MXMOE_EUNSUPPORTED, "window = %d exceeds 2^30", window);
   if (!(scale >= -1e30f && scale <= 1e30f)) return fail(MXMOE_EINVAL, "scale must be finite (at most 1e30)");
   if (B == 0) return MXMOE_OK;
+  // the work is counted in 32 bits: units of 32 keys or more, per key/value head and 8 rows
+  const int64_t row_tiles = mxmoe::cdiv(static_cast<int64_t>(Hq / Hkv) * Lq, 8);
+  if (static_cast<double>(B) * Hkv * static_cast<double>(row_tiles) * (static_cast<double>(max_pages) * page_size / 32 + 1) >= 2147483648.0)
+    return fail(MXMOE_EUNSUPPORTED, "B = %d sequences of up to %d pages are too much for one call", B, max_pages);
   if (ldq < static_cast<int64_t>(Hq) * D || ldq % 8)
     return fail(MXMOE_EINVAL, "ldq must be a multiple of 8 and at least Hq * D = %lld", (long long)Hq * D);
   if (!q || !seq_lens || !out || !workspace || (max_pages > 0 && !block_table) ||
@@ -1310,9 +1314,10 @@ int mxfp4_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* k_blocks, 
   a.scale_sign = scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f;
   a.out = out;
   a.err = ws->err;
-  cudaError_t e = mxmoe::launch_kv_attention(a, workspace, ws->sms, static_cast<cudaStream_t>(stream));
+  int launches = 0;
+  cudaError_t e = mxmoe::launch_kv_attention(a, workspace, ws->sms, static_cast<cudaStream_t>(stream), &launches);
   if (e) return cuda_fail(e, "kv attention launch");
-  t_last_launches = 2;
+  t_last_launches = launches;
   return MXMOE_OK;
 }
 

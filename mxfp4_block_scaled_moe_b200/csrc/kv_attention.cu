@@ -54,7 +54,8 @@ struct Shape {
   static constexpr int kSc = kUnit * kBlocks;          // their scales
   static constexpr int kStageBytes = 2 * kKV + 2 * kSc + 16;
   static constexpr int kStages = 3;
-  static constexpr int kSmem = kWarps * kStages * kStageBytes;
+  static constexpr int kFactors = 2 * kBlocks * kUnit * 4;   // a unit's scales as fp32, keys' and values'
+  static constexpr int kSmem = kWarps * (kStages * kStageBytes + kFactors);
   static constexpr int kCtas = D == 64 || NT == 1 ? 2 : 1;   // per SM, by registers
 };
 
@@ -87,6 +88,31 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// pairs of fp32: one instruction for both halves, half the issue slots of the scalar forms
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo_of(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi_of(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -113,12 +139,26 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 __device__ __forceinline__ uint32_t lds32(const uint8_t* at) { return *reinterpret_cast<const uint32_t*>(at); }
-__device__ __forceinline__ uint32_t lds16(const uint8_t* at) { return *reinterpret_cast<const uint16_t*>(at); }
 // the scale bytes of a key's blocks (2 or 4 of them), at `at`
 template <int kBlocks>
 __device__ __forceinline__ uint32_t lds_scales(const uint8_t* at) {
   if constexpr (kBlocks == 4) return lds32(at);
-  return lds16(at);
+  return *reinterpret_cast<const uint16_t*>(at);
+}
+// Four 8 x 16-byte matrices whose rows lie at the lanes' addresses (lanes 8 i .. 8 i + 7: matrix
+// i). Plain: r[i] is word t of row g. Transposed: the 16-bit elements g of rows 2t (low) and
+// 2t + 1.
+__device__ __forceinline__ void ldmatrix(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
 }
 // byte k of a word as the exponent field of an fp32: 2^(byte - 127). Byte 0 reads as zero: its
 // block's values are below 2^-124.
@@ -148,24 +188,28 @@ __device__ __forceinline__ int units_of(const KvAttentionArgs& p, int len) {
   return max(1, (len - first + kUnit - 1) / kUnit);   // an empty sequence still writes its zeros
 }
 
-// Position in the line of units: an item (key/value head h, row tile rt of sequence b), its
-// first unit relative to the warp's run, its units.
+// Position in the line of units, counted from the warp's run: an item (key/value head h, row
+// tile rt of sequence b), the unit behind its last and the key that unit 0 of the run would
+// start at if it were the item's.
 template <int kUnit>
 struct Cursor {
-  int b, h, rt, len, first, units, start;
-  __device__ void load(const KvAttentionArgs& p) {
+  int b, h, rt, len, end, key0;
+  __device__ void open(const KvAttentionArgs& p, int start) {   // b, h, rt set; the item starts at unit `start`
     len = seq_len(p, b);
-    first = first_seen(p, len);
-    units = units_of<kUnit>(p, len);
+    const int first = first_seen(p, len) & ~(kUnit - 1);
+    end = start + max(1, (len - first + kUnit - 1) / kUnit);
+    key0 = first - kUnit * start;
   }
-  __device__ int key(int unit) const { return (first & ~(kUnit - 1)) + kUnit * (unit - start); }
+  __device__ int key(int unit) const { return key0 + kUnit * unit; }
   __device__ void next(const KvAttentionArgs& p) {
-    start += units;
-    if (++rt < p.RT) return;
-    rt = 0;
-    if (++h < p.Hkv) return;
-    h = 0;
-    if (++b < p.B) load(p);
+    if (++rt == p.RT) {
+      rt = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        if (++b == p.B) return;
+      }
+    }
+    open(p, end);
   }
 };
 
@@ -173,73 +217,88 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_kernel(const KvAttentionArgs p) {
   using S = Shape<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_sum[kWarps];
-  __shared__ int64_t s_pre[kThreads];
+  __shared__ int s_sum[kWarps];
+  __shared__ int s_pre[kThreads];
+  __shared__ int s_per;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int per_seq = p.Hkv * p.RT;
   griddep_launch_dependents();   // the joining kernel may take its places; it waits for this one's end
 
-  // ---- this warp's run: units [t0, t0 + count) of n ----
+  // ---- this warp's run: `count` units from `cur` on, whose item may have begun before it ----
   // neighbouring runs go to different SMs, so that a short line still uses all of them
-  const int run = warp * gridDim.x + blockIdx.x;
-  int64_t per = 0, t0 = 0;
-  int count = 0;
+  const int run = warp * gridDim.x + blockIdx.x, runs = gridDim.x * kWarps;
+  int count = 0, start = 0;   // start: of the run's first item, in the run
   Cursor<S::kUnit> cur;
   cur.b = -1;
-  // pass 0 counts the line's units, pass 1 finds the run's first; a batch of one chunk of
-  // kThreads sequences needs its prefix sums once
-  for (int pass = p.B > kThreads ? 0 : 1; pass < 2; ++pass) {
-    int64_t base = 0;   // units before this chunk of sequences
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      const int64_t u = b < p.B ? static_cast<int64_t>(units_of<S::kUnit>(p, seq_len(p, b))) * per_seq : 0;
-      int64_t pre = u;   // inclusive over the warp
+  if (p.whole) {
+    const int items = p.B * per_seq, each = (items + runs - 1) / runs;
+    const int i0 = run * each, i1 = min(items, i0 + each);
+    for (int i = i0 + lane; i < i1; i += 32) count += units_of<S::kUnit>(p, seq_len(p, i / per_seq));
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (count > 0) {
+      cur.b = i0 / per_seq;
+      cur.h = i0 % per_seq / p.RT;
+      cur.rt = i0 % p.RT;
+      cur.open(p, 0);
+    }
+  } else {
+    // pass 0 counts the line's units, pass 1 finds the run's first; a batch of one chunk of
+    // kThreads sequences needs its prefix sums once
+    int per = 0, t0 = 0;
+    for (int pass = p.B > kThreads ? 0 : 1; pass < 2; ++pass) {
+      int base = 0;   // units before this chunk of sequences
+      for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int pre = b < p.B ? units_of<S::kUnit>(p, seq_len(p, b)) * per_seq : 0;   // inclusive over the warp
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += x;
-      }
-      __syncthreads();   // s_sum and s_pre of the step before have been read
-      if (lane == 31) s_sum[warp] = pre;
-      __syncthreads();
-      int64_t all = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += x;
+        }
+        __syncthreads();   // s_sum and s_pre of the step before have been read
+        if (lane == 31) s_sum[warp] = pre;
+        __syncthreads();
+        int all = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) pre += s_sum[w];
-        all += s_sum[w];
-      }
-      s_pre[threadIdx.x] = base + pre;
-      __syncthreads();
-      if (pass == 0 || p.B <= kThreads) {
-        const int64_t n = base + all, runs = static_cast<int64_t>(gridDim.x) * kWarps;
-        per = max(static_cast<int64_t>(64 / S::kUnit), (n + runs - 1) / runs);   // 64 keys at least
-        t0 = per * run;
-        count = static_cast<int>(max(static_cast<int64_t>(0), min(per, n - t0)));
-      }
-      if (pass == 1 && count > 0 && base <= t0 && t0 < base + all) {
-        // the first sequence of the chunk whose units end after t0
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) pre += s_sum[w];
+          all += s_sum[w];
+        }
+        s_pre[threadIdx.x] = base + pre;
+        __syncthreads();
+        if (pass == 0 || p.B <= kThreads) {
+          const int n = base + all;
+          per = max(64 / S::kUnit, n / runs + (n % runs ? 1 : 0));   // 64 keys at least
+          t0 = static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(per) * run));
+          count = min(per, n - t0);
+        }
+        if (pass == 1 && count > 0 && base <= t0 && t0 < base + all) {
+          // the first sequence of the chunk whose units end after t0
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) {
-          const unsigned past = __ballot_sync(0xffffffffu, s_pre[32 * i + lane] > t0);
-          if (past && cur.b < 0) {
-            const int at = 32 * i + __ffs(past) - 1;
-            cur.b = b0 + at;
-            cur.load(p);
-            const int64_t from = s_pre[at] - static_cast<int64_t>(cur.units) * per_seq;
-            const int j = static_cast<int>((t0 - from) / cur.units);
-            cur.h = j / p.RT;
-            cur.rt = j % p.RT;
-            cur.start = static_cast<int>(from + static_cast<int64_t>(j) * cur.units - t0);
+          for (int i = 0; i < kThreads / 32; ++i) {
+            const unsigned past = __ballot_sync(0xffffffffu, s_pre[32 * i + lane] > t0);
+            if (past && cur.b < 0) {
+              const int at = 32 * i + __ffs(past) - 1;
+              cur.b = b0 + at;
+              const int units = units_of<S::kUnit>(p, seq_len(p, cur.b));
+              const int into = t0 - (s_pre[at] - units * per_seq), j = into / units;
+              cur.h = j / p.RT;
+              cur.rt = j % p.RT;
+              start = j * units - into;
+              cur.open(p, start);
+            }
           }
         }
+        base += all;
       }
-      base += all;
     }
+    if (threadIdx.x == 0) s_per = per;
+    __syncthreads();
   }
   if (count == 0) return;
 
   // ---- this warp's ring of units ----
-  uint8_t* const ring = smem + warp * S::kStages * S::kStageBytes;
+  uint8_t* const ring = smem + warp * (S::kStages * S::kStageBytes + S::kFactors);
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   constexpr int kPages = 2 * S::kKV + 2 * S::kSc;   // offset of a stage's flags: which 16 keys were loaded
   constexpr int kChunks = S::kRowBytes / 16;        // 16-byte chunks of a row, one MXFP4 block each
@@ -259,9 +318,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
   bool in_need = false;
   auto look = [&]() {
     if (in_unit >= count) return;
-    if (in_unit >= in.start + in.units) in.next(p);
+    if (in_unit >= in.end) in.next(p);
     const int key = in.key(in_unit) + 16 * lane;
-    in_need = lane < S::kTiles && key < in.len && key + 16 > in.first;   // keys that no query sees need no page
+    // keys that no query sees need no page
+    in_need = lane < S::kTiles && key < in.len && key + 16 > first_seen(p, in.len);
     if (in_need) pid = __ldg(p.block_table + static_cast<int64_t>(in.b) * p.max_pages + (key >> p.page_shift));
   };
   auto issue = [&](int stage) {
@@ -315,14 +375,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
 #pragma unroll
   for (int s = 0; s < S::kStages - 1; ++s) issue(s);
 
-  // where the lane's operands lie in a stage: words of keys g (+ 8, + 16, ...), of values 2t (+ ...)
-  const uint32_t get_k = g * S::kRowBytes + 16 * (kChunks == 2 ? (g >> 2) & 1 : (g >> 1) & 3) + 4 * t;
-  const uint32_t get_v = 2 * t * S::kRowBytes + 16 * (kChunks == 2 ? (t >> 1) & 1 : t) + 4 * (g & 3) + 2 * (g >> 2);
+  // The lane's row of an operand load of 16 keys and two blocks (matrices: keys 0-7 and 8-15 of
+  // the first, of the second), alike for keys and values.
+  const uint32_t get = (lane & 15) * S::kRowBytes +
+                       16 * ((lane >> 4) ^ (kChunks == 2 ? (lane >> 2) & 1 : (lane >> 1) & 3));
+  float* const factors = reinterpret_cast<float*>(ring + S::kStages * S::kStageBytes);   // [key][keys' blocks, values']
 
   int stage = 0;
   for (int at = 0; at < count;) {
     // ---- one item: rows, queries ----
-    const int item_end = cur.start + cur.units, end = min(count, item_end);
+    const int end = min(count, cur.end), from = at;
     const int len = cur.len, h = cur.h, row0 = cur.rt * S::kRows;
     uint32_t qf[NT][S::kBlocks][4];
     float qs[NT][2];                      // of rows 2t, 2t + 1: score scale in base 2, undoing the f16 shift
@@ -368,7 +430,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
 
     float o[NT][S::kBlocks][2][4];
     float m[NT][2], l[NT][2];   // m before the row's factor, so that the largest weight is exactly 1
-    float base[NT][2], vf[S::kBlocks];
     int E[S::kBlocks];   // as an fp32's exponent field
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -377,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[i][k][0][x] = o[i][k][1][x] = 0.f;
       m[i][0] = m[i][1] = -INFINITY;
-      l[i][0] = l[i][1] = base[i][0] = base[i][1] = 0.f;
+      l[i][0] = l[i][1] = 0.f;
     }
 #pragma unroll
     for (int k = 0; k < S::kBlocks; ++k) E[k] = 0;
@@ -387,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
       cp_async_wait<S::kStages - 2>();
       __syncwarp();
       const uint8_t* sk = ring + stage * S::kStageBytes;
+      const uint32_t sk_at = ring_at + stage * S::kStageBytes;
       const uint8_t *ssk = sk + 2 * S::kKV, *ssv = ssk + S::kSc;
       {
         const int next = stage + S::kStages - 1;
@@ -396,96 +458,128 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
       const unsigned pages = lds32(sk + kPages);
       const int key0 = cur.key(at);
 
-      // scores, before the row's factor
-      float s[NT][S::kTiles][4];
-      float kf[S::kBlocks];   // the scales of the lane's key of 32
+      // The unit's scales as fp32: the keys' own, the values' as weight factors 2^(15 + e - E). A
+      // lane takes keys lane (and lane + 32). A key that no row sees counts as scale 0: what
+      // lies in its place does not matter.
+      const bool edge = pages != (1u << S::kTiles) - 1 || key0 < full_lo || key0 + S::kUnit > full_hi;
+      uint32_t sc[S::kUnit / 32], ev[S::kUnit / 32], top[S::kBlocks];
 #pragma unroll
-      for (int y = 0; y < S::kTiles; ++y) {
-        if (y % 2 == 0) {
-          const uint32_t sc = lds_scales<S::kBlocks>(ssk + (16 * y + lane) * S::kBlocks);
-#pragma unroll
-          for (int k = 0; k < S::kBlocks; ++k) kf[k] = __uint_as_float(exponent_of(sc, k));
+      for (int e = 0; e < S::kUnit / 32; ++e) {
+        sc[e] = lds_scales<S::kBlocks>(ssk + (32 * e + lane) * S::kBlocks);
+        ev[e] = lds_scales<S::kBlocks>(ssv + (32 * e + lane) * S::kBlocks);
+        if (edge) {
+          const int key = key0 + 32 * e + lane;
+          if (key < seen_lo || key >= seen_hi || !((pages >> (2 * e + (lane >> 4))) & 1)) ev[e] = 0;
         }
+      }
+      bool higher = false;
+#pragma unroll
+      for (int k = 0; k < S::kBlocks; ++k) {
+        top[k] = exponent_of(ev[0], k);
+#pragma unroll
+        for (int e = 1; e < S::kUnit / 32; ++e) top[k] = max(top[k], exponent_of(ev[e], k));
+        higher |= static_cast<int>(top[k]) > E[k];
+      }
+      if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k) {
-          uint32_t a[4], b[4];
-          expand(lds32(sk + (get_k ^ (16 * k)) + 16 * y * S::kRowBytes), a);
-          expand(lds32(sk + (get_k ^ (16 * k)) + (16 * y + 8) * S::kRowBytes), b);
-          const float fa = __shfl_sync(0xffffffffu, kf[k], 16 * (y % 2) + g);
-          const float fb = __shfl_sync(0xffffffffu, kf[k], 16 * (y % 2) + g + 8);
+          const int e = max(E[k], static_cast<int>(__reduce_max_sync(0xffffffffu, top[k])));
+          const float f = ex2(static_cast<float>((E[k] - e) >> 23));
+          E[k] = e;
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            float c[4];
-            mma_f16_zero(c, a[0], b[0], a[1], b[1], qf[i][k][0], qf[i][k][1]);
-            mma_f16(c, a[2], b[2], a[3], b[3], qf[i][k][2], qf[i][k][3]);
-            if (k == 0) {
-              s[i][y][0] = c[0] * fa;
-              s[i][y][1] = c[1] * fa;
-              s[i][y][2] = c[2] * fb;
-              s[i][y][3] = c[3] * fb;
-            } else {
-              s[i][y][0] = fmaf(c[0], fa, s[i][y][0]);
-              s[i][y][1] = fmaf(c[1], fa, s[i][y][1]);
-              s[i][y][2] = fmaf(c[2], fb, s[i][y][2]);
-              s[i][y][3] = fmaf(c[3], fb, s[i][y][3]);
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              o[i][k][0][x] *= f;
+              o[i][k][1][x] *= f;
+            }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < S::kUnit / 32; ++e) {
+        float f[2 * S::kBlocks];
+#pragma unroll
+        for (int k = 0; k < S::kBlocks; ++k) {
+          f[k] = __uint_as_float(exponent_of(sc[e], k));
+          f[S::kBlocks + k] = __int_as_float(max(static_cast<int>(exponent_of(ev[e], k)) - E[k] + (142 << 23), 0));
+        }
+#pragma unroll
+        for (int k = 0; k < 2 * S::kBlocks; k += 4)
+          *reinterpret_cast<float4*>(factors + (32 * e + lane) * 2 * S::kBlocks + k) =
+              make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+      }
+      __syncwarp();
+
+      // scores, before the row's factor
+      f32x2 s[NT][S::kTiles][2];   // keys g, g + 8 of a tile; rows 2t, 2t + 1
+#pragma unroll
+      for (int y = 0; y < S::kTiles; ++y) {
+        const float* fa = factors + (16 * y + g) * 2 * S::kBlocks;
+        const float* fb = fa + 8 * 2 * S::kBlocks;
+#pragma unroll
+        for (int k2 = 0; k2 < S::kBlocks; k2 += 2) {
+          uint32_t w[4];
+          ldmatrix(sk_at + (get ^ (16 * k2)) + 16 * y * S::kRowBytes, w);
+          const float2 ka = *reinterpret_cast<const float2*>(fa + k2), kb = *reinterpret_cast<const float2*>(fb + k2);
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            const int k = k2 + kk;
+            uint32_t a[4], b[4];
+            expand(w[2 * kk], a);
+            expand(w[2 * kk + 1], b);
+            const f32x2 f0 = kk ? pair(ka.y, ka.y) : pair(ka.x, ka.x), f1 = kk ? pair(kb.y, kb.y) : pair(kb.x, kb.x);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              float c[4];
+              mma_f16_zero(c, a[0], b[0], a[1], b[1], qf[i][k][0], qf[i][k][1]);
+              mma_f16(c, a[2], b[2], a[3], b[3], qf[i][k][2], qf[i][k][3]);
+              if (k == 0) {
+                s[i][y][0] = mul2(pair(c[0], c[1]), f0);
+                s[i][y][1] = mul2(pair(c[2], c[3]), f1);
+              } else {
+                s[i][y][0] = fma2(pair(c[0], c[1]), f0, s[i][y][0]);
+                s[i][y][1] = fma2(pair(c[2], c[3]), f1, s[i][y][1]);
+              }
             }
           }
         }
       }
-      // the value scales of the lane's keys (lane, lane + 32), 0 for a key that no row sees (what
-      // lies there does not count)
-      uint32_t ev[S::kUnit / 32];
+      if (edge) {
 #pragma unroll
-      for (int e = 0; e < S::kUnit / 32; ++e) ev[e] = lds_scales<S::kBlocks>(ssv + (32 * e + lane) * S::kBlocks);
-      if (pages != (1u << S::kTiles) - 1 || key0 < full_lo || key0 + S::kUnit > full_hi) {
-#pragma unroll
-        for (int e = 0; e < S::kUnit / 32; ++e) {
-          const int key = key0 + 32 * e + lane;
-          if (key < seen_lo || key >= seen_hi || !((pages >> (2 * e + (lane >> 4))) & 1)) ev[e] = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < NT; ++i) {
+          int hi[2], lo[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int row = row0 + 8 * i + 2 * t + x;
-            const int hi = row < p.R ? len - p.Lq + row / p.G + 1 : 0, lo = p.window > 0 ? hi - p.window : 0;
-#pragma unroll
-            for (int y = 0; y < S::kTiles; ++y) {
-              const int ka = key0 + 16 * y + g;
-              const bool gone = !((pages >> y) & 1);
-              if (gone || ka < lo || ka >= hi) s[i][y][x] = -INFINITY;
-              if (gone || ka + 8 < lo || ka + 8 >= hi) s[i][y][x + 2] = -INFINITY;
-            }
+            hi[x] = row < p.R ? len - p.Lq + row / p.G + 1 : 0;
+            lo[x] = p.window > 0 ? hi[x] - p.window : 0;
           }
+#pragma unroll
+          for (int y = 0; y < S::kTiles; ++y)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int key = key0 + 16 * y + 8 * z + g;
+              const bool gone = !((pages >> y) & 1);
+              s[i][y][z] = pair(gone || key < lo[0] || key >= hi[0] ? -INFINITY : lo_of(s[i][y][z]),
+                                gone || key < lo[1] || key >= hi[1] ? -INFINITY : hi_of(s[i][y][z]));
+            }
+        }
       }
       // does a maximum grow?
       float mx[NT][2];
       bool grows = false;
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < NT; ++i) {
+        mx[i][0] = fmaxf(lo_of(s[i][0][0]), lo_of(s[i][0][1]));
+        mx[i][1] = fmaxf(hi_of(s[i][0][0]), hi_of(s[i][0][1]));
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          mx[i][x] = fmaxf(s[i][0][x], s[i][0][x + 2]);
-#pragma unroll
-          for (int y = 1; y < S::kTiles; ++y) mx[i][x] = fmaxf(mx[i][x], fmaxf(s[i][y][x], s[i][y][x + 2]));
-          grows |= mx[i][x] > m[i][x];
+        for (int y = 1; y < S::kTiles; ++y) {
+          mx[i][0] = fmaxf(mx[i][0], fmaxf(lo_of(s[i][y][0]), lo_of(s[i][y][1])));
+          mx[i][1] = fmaxf(mx[i][1], fmaxf(hi_of(s[i][y][0]), hi_of(s[i][y][1])));
         }
-      uint32_t top[S::kBlocks];
-#pragma unroll
-      for (int k = 0; k < S::kBlocks; ++k) {
-        top[k] = 0;
-#pragma unroll
-        for (int e = 0; e < S::kUnit / 32; ++e) top[k] = max(top[k], exponent_of(ev[e], k));
-        grows |= static_cast<int>(top[k]) > E[k];
+        grows |= mx[i][0] > m[i][0] || mx[i][1] > m[i][1];
       }
       if (__any_sync(0xffffffffu, grows)) {
-        float dE[S::kBlocks];
-#pragma unroll
-        for (int k = 0; k < S::kBlocks; ++k) {
-          const int e = max(E[k], static_cast<int>(__reduce_max_sync(0xffffffffu, top[k])));
-          dE[k] = static_cast<float>((E[k] - e) >> 23);
-          E[k] = e;
-        }
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -495,13 +589,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             const float nm = fmaxf(m[i][x], v);
-            const float d = nm == -INFINITY ? 0.f : (m[i][x] - nm) * qs[i][x];   // nothing seen yet: all zero anyway
+            // nothing seen yet: all zero anyway
+            const float f = nm == -INFINITY ? 1.f : ex2((m[i][x] - nm) * qs[i][x]);
             m[i][x] = nm;
-            base[i][x] = nm == -INFINITY ? 0.f : nm;
-            l[i][x] *= ex2(d);
+            l[i][x] *= f;
 #pragma unroll
             for (int k = 0; k < S::kBlocks; ++k) {
-              const float f = ex2(d + dE[k]);
               o[i][k][0][x] *= f;
               o[i][k][0][x + 2] *= f;
               o[i][k][1][x] *= f;
@@ -510,44 +603,52 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
           }
       }
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < NT; ++i) {
+        const f32x2 base = pair(m[i][0] == -INFINITY ? 0.f : -m[i][0], m[i][1] == -INFINITY ? 0.f : -m[i][1]);
+        const f32x2 q2 = pair(qs[i][0], qs[i][1]);
+        f32x2 sum = pair(l[i][0], l[i][1]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int y = 0; y < S::kTiles; ++y)
 #pragma unroll
-          for (int y = 0; y < S::kTiles; ++y) {
-            s[i][y][x] = ex2((s[i][y][x] - base[i][x]) * qs[i][x]);
-            s[i][y][x + 2] = ex2((s[i][y][x + 2] - base[i][x]) * qs[i][x]);
-            l[i][x] += s[i][y][x] + s[i][y][x + 2];
+          for (int z = 0; z < 2; ++z) {
+            const f32x2 e = mul2(add2(s[i][y][z], base), q2);
+            s[i][y][z] = pair(ex2(lo_of(e)), ex2(hi_of(e)));
+            sum = add2(sum, s[i][y][z]);
           }
+        l[i][0] = lo_of(sum);
+        l[i][1] = hi_of(sum);
+      }
       // O^T += V^T P^T
 #pragma unroll
       for (int y = 0; y < S::kTiles; ++y) {
-        if (y % 2 == 0) {
-          // the weight factors 2^(15 + e - E) in [0, 2^15] of the lane's key of these 32
+        const float* fa = factors + (16 * y + g) * 2 * S::kBlocks + S::kBlocks;
+        const float* fb = fa + 8 * 2 * S::kBlocks;
 #pragma unroll
-          for (int k = 0; k < S::kBlocks; ++k)
-            vf[k] = __int_as_float(max(static_cast<int>(exponent_of(ev[y / 2], k)) - E[k] + (142 << 23), 0));
-        }
+        for (int k2 = 0; k2 < S::kBlocks; k2 += 2) {
+          uint32_t w[4];   // [2 kk + z]: columns 4g .. 4g + 3 of keys 8z + 2t (low half), 8z + 2t + 1
+          ldmatrix_trans(sk_at + S::kKV + (get ^ (16 * k2)) + 16 * y * S::kRowBytes, w);
+          const float2 va = *reinterpret_cast<const float2*>(fa + k2), vb = *reinterpret_cast<const float2*>(fb + k2);
 #pragma unroll
-        for (int k = 0; k < S::kBlocks; ++k) {
-          const float fa = __shfl_sync(0xffffffffu, vf[k], 16 * (y % 2) + g);
-          const float fb = __shfl_sync(0xffffffffu, vf[k], 16 * (y % 2) + g + 8);
-          const uint8_t* v0 = sk + S::kKV + (get_v ^ (16 * k)) + 16 * y * S::kRowBytes;
-          // pair the keys' codes of one column in a byte: columns 0, 2 in `even`, 1, 3 in `odd`;
-          // bytes 0, 1 of keys (2t, 2t + 1), bytes 2, 3 of keys (2t + 8, 2t + 9)
-          const uint32_t first = lds16(v0) + lds16(v0 + 8 * S::kRowBytes) * 65536u;
-          const uint32_t second = lds16(v0 + S::kRowBytes) + lds16(v0 + 9 * S::kRowBytes) * 65536u;
-          const uint32_t even = (first & 0x0F0F0F0Fu) | ((second << 4) & 0xF0F0F0F0u);
-          const uint32_t odd = ((first >> 4) & 0x0F0F0F0Fu) | (second & 0xF0F0F0F0u);
-          uint32_t ae[4], ao[4];
-          expand(even, ae);
-          expand(odd, ao);
+          for (int kk = 0; kk < 2; ++kk) {
+            const int k = k2 + kk;
+            // pair the keys' codes of one column in a byte: columns 0, 2 in `even`, 1, 3 in `odd`;
+            // bytes 0, 1 of keys (2t, 2t + 1), bytes 2, 3 of keys (2t + 8, 2t + 9)
+            const uint32_t first = __byte_perm(w[2 * kk], w[2 * kk + 1], 0x5410);
+            const uint32_t second = __byte_perm(w[2 * kk], w[2 * kk + 1], 0x7632);
+            const uint32_t even = (first & 0x0F0F0F0Fu) | ((second << 4) & 0xF0F0F0F0u);
+            const uint32_t odd = ((first >> 4) & 0x0F0F0F0Fu) | (second & 0xF0F0F0F0u);
+            uint32_t ae[4], ao[4];
+            expand(even, ae);
+            expand(odd, ao);
+            const f32x2 f0 = kk ? pair(va.y, va.y) : pair(va.x, va.x), f1 = kk ? pair(vb.y, vb.y) : pair(vb.x, vb.x);
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const uint32_t b0 = transpose8x8(pack_f16(s[i][y][0] * fa, s[i][y][1] * fa));
-            const uint32_t b1 = transpose8x8(pack_f16(s[i][y][2] * fb, s[i][y][3] * fb));
-            mma_f16(o[i][k][0], ae[0], ao[0], ae[2], ao[2], b0, b1);
-            mma_f16(o[i][k][1], ae[1], ao[1], ae[3], ao[3], b0, b1);
+            for (int i = 0; i < NT; ++i) {
+              const f32x2 wa = mul2(s[i][y][0], f0), wb = mul2(s[i][y][1], f1);
+              const uint32_t b0 = transpose8x8(pack_f16(lo_of(wa), hi_of(wa)));
+              const uint32_t b1 = transpose8x8(pack_f16(lo_of(wb), hi_of(wb)));
+              mma_f16(o[i][k][0], ae[0], ao[0], ae[2], ao[2], b0, b1);
+              mma_f16(o[i][k][1], ae[1], ao[1], ae[3], ao[3], b0, b1);
+            }
           }
         }
       }
@@ -555,8 +656,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
     }
 
     // ---- the item's end in this run ----
-    const bool whole = cur.start >= 0 && item_end <= count;
-    const int64_t slot = 2 * static_cast<int64_t>(run) + (cur.start > 0 ? 1 : 0);
+    const bool opened = from > 0 || start == 0;   // the item's first unit is in this run
+    const bool whole = opened && cur.end <= count;
+    const int64_t slot = 2 * static_cast<int64_t>(run) + (from > 0 ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -566,10 +668,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int r = 8 * i + 2 * t + x, row = row0 + r;
-        const int c0 = 8 * (g & 3) + 4 * (g >> 2);   // the lane's four columns of a block
+        const int c0 = 4 * g;   // the lane's four columns of a block
         if (row < p.R && whole) {
           const int hd = h * p.G + row % p.G;
-          if (p.sinks) sum += ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base[i][x] * qs[i][x]);
+          const float base = m[i][x] == -INFINITY ? 0.f : m[i][x] * qs[i][x];
+          if (p.sinks) sum += ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base);
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
           uint16_t* dst = p.out + ((static_cast<int64_t>(cur.b) * p.Lq + row / p.G) * p.Hkv * p.G + hd) * D + c0;
 #pragma unroll
@@ -592,12 +695,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
       }
     // the run that holds the item's first unit says where its parts lie (slot, first and last
     // run); -1: no parts
-    if (lane == 0 && cur.start >= 0) {
+    if (lane == 0 && opened && !p.whole) {
       const int64_t item = (static_cast<int64_t>(cur.b) * p.Hkv + h) * p.RT + cur.rt;
       p.desc[item] = whole ? make_int4(-1, 0, 0, 0)
-                           : make_int4(static_cast<int>(slot), run, static_cast<int>((t0 + item_end - 1) / per), 0);
+                           : make_int4(static_cast<int>(slot), run, run + (cur.end - 1) / s_per, 0);
     }
-    if (at == item_end && at < count) cur.next(p);
+    if (at == cur.end && at < count) cur.next(p);
   }
   cp_async_wait<0>();
 }
@@ -693,14 +796,21 @@ Layout layout(int64_t items, int R, int D, int sms) {
 }
 
 template <int D, int NT>
-cudaError_t launch(KvAttentionArgs p, int sms, cudaStream_t st) {
+cudaError_t launch(KvAttentionArgs p, int sms, cudaStream_t st, int* launches) {
   using namespace kva;
   using S = Shape<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(kv_attention_kernel<D, NT>, S::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = sms * S::kCtas;
+  // Items of at most four units (a short window or a short table) are not cut: a warp takes
+  // them whole, nothing is left to join, and no run has to be found.
+  const int64_t keys = static_cast<int64_t>(p.max_pages) << p.page_shift;
+  const int64_t reach = p.window > 0 ? std::min<int64_t>(keys, static_cast<int64_t>(p.window) + p.Lq - 1) : keys;
+  p.whole = cdiv(reach, S::kUnit) + (reach < keys ? 1 : 0) <= 4;
+  *launches = p.whole ? 1 : 2;
   kv_attention_kernel<D, NT><<<grid, kThreads, S::kSmem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || p.whole) return e;
   // Few items are cut into many parts each: a CTA per row, its warps over the parts.
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * p.RT;
   const int rows = items < 2 * sms ? 1 : S::kRows;
@@ -723,7 +833,7 @@ size_t kv_attention_workspace(int B, int Lq, int Hq, int Hkv, int D, int sms) {
   return layout(static_cast<int64_t>(B) * Hkv * cdiv(R, 8 * tiles_n(R)), R, D, sms).bytes;
 }
 
-cudaError_t launch_kv_attention(KvAttentionArgs p, void* workspace, int sms, cudaStream_t st) {
+cudaError_t launch_kv_attention(KvAttentionArgs p, void* workspace, int sms, cudaStream_t st, int* launches) {
   const int nt = tiles_n(p.R);
   p.RT = static_cast<int>(cdiv(p.R, 8 * nt));
   const Layout l = layout(static_cast<int64_t>(p.B) * p.Hkv * p.RT, p.R, p.D, sms);
@@ -731,8 +841,8 @@ cudaError_t launch_kv_attention(KvAttentionArgs p, void* workspace, int sms, cud
   p.desc = reinterpret_cast<int4*>(base + l.desc);
   p.part_ml = reinterpret_cast<float2*>(base + l.ml);
   p.part = reinterpret_cast<float*>(base + l.part);
-  if (p.D == 64) return nt == 1 ? launch<64, 1>(p, sms, st) : launch<64, 2>(p, sms, st);
-  return nt == 1 ? launch<128, 1>(p, sms, st) : launch<128, 2>(p, sms, st);
+  if (p.D == 64) return nt == 1 ? launch<64, 1>(p, sms, st, launches) : launch<64, 2>(p, sms, st, launches);
+  return nt == 1 ? launch<128, 1>(p, sms, st, launches) : launch<128, 2>(p, sms, st, launches);
 }
 
 }  // namespace mxmoe

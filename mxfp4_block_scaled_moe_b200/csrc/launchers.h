@@ -1,10 +1,31 @@
 // Host-side launchers of the library's kernels (internal; the public ABI is mxfp4_moe.h).
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace mxmoe {
+
+// Raises a kernel's dynamic shared-memory limit, once per device (one static object a kernel).
+class SmemLimit {
+ public:
+  template <class Kernel>
+  cudaError_t raise(Kernel kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && done_[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) done_[dev].store(true, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<bool> done_[64] = {};
+};
 
 cudaError_t launch_quantize(const float* w, int64_t rows, int64_t K, uint8_t* blocks,
                             uint8_t* scales, cudaStream_t st, int sms);
@@ -228,8 +249,8 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
 
-// attention over that cache (csrc/kv_attention.cu): D 64 or 128. launch_kv_attention sets RT
-// and the workspace pointers.
+// attention over that cache (csrc/kv_attention.cu): D 64 or 128. launch_kv_attention sets RT,
+// whole and the workspace pointers.
 struct KvAttentionArgs {
   const uint16_t* q;
   int64_t q_stride;             // elements between tokens
@@ -249,12 +270,13 @@ struct KvAttentionArgs {
   uint16_t* out;                // (B, Lq, Hkv * G, D)
   int* err;
   int RT;                       // row tiles of an item
+  int whole;                    // items are not cut over warps
   int4* desc;
   float2* part_ml;
   float* part;
 };
 size_t kv_attention_workspace(int B, int Lq, int Hq, int Hkv, int D, int sms);
-cudaError_t launch_kv_attention(KvAttentionArgs a, void* workspace, int sms, cudaStream_t st);
+cudaError_t launch_kv_attention(KvAttentionArgs a, void* workspace, int sms, cudaStream_t st, int* launches);
 
 // FP8 linear on E4M3 codes with a fused epilogue (csrc/linear_fused_sm100.cu)
 struct LinearFusedArgs {

@@ -506,8 +506,8 @@ cudaError_t launch_pair(const LinearFusedArgs& p, int sms, cudaStream_t st) {
   using namespace linf;
   CUtensorMap mx, mw;
   if (!encode_codes(&mx, p.xq, p.T, p.K, 128) || !encode_codes(&mw, p.wq, p.N, p.K, 128)) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(fp8_linear_pair_kernel<kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       pair::kSmemBytes);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(fp8_linear_pair_kernel<kAct>, pair::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int64_t units = cdiv(p.T, pair::BM) * cdiv(p.N, pair::BN);
   const int grid = 2 * static_cast<int>(std::min<int64_t>(units, sms / 2));
@@ -541,7 +541,8 @@ cudaError_t launch_split(const LinearFusedArgs& p, int sms, cudaStream_t st) {
   CUtensorMap mx, mw;
   if (!encode_codes(&mx, p.xq, p.T, p.K, BN) || !encode_codes(&mw, p.wq, p.N, p.K, split::BM)) return cudaErrorInvalidValue;
   constexpr int smem = split::smem_bytes(BN);
-  cudaError_t e = cudaFuncSetAttribute(fp8_linear_split_kernel<BN, kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(fp8_linear_split_kernel<BN, kAct>, smem);
   if (e != cudaSuccess) return e;
   const int m_tiles = static_cast<int>(cdiv(p.N, split::BM)), t_tiles = static_cast<int>(cdiv(p.T, BN));
   const int nk = static_cast<int>(cdiv(p.K, BK));
