@@ -712,8 +712,9 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const KvAttentionArgs p, int rows) {
   using S = Shape<D, NT>;
   constexpr int kCols = D / 32;   // columns of a lane
-  __shared__ float s_o[kJoinThreads / 32][D];
-  __shared__ float2 s_ml[kJoinThreads / 32];
+  extern __shared__ __align__(16) uint8_t smem[];   // one-row sets only: a CTA without any fits beside the kernel before
+  float(*const s_o)[D] = reinterpret_cast<float(*)[D]>(smem);
+  float* const s_l = reinterpret_cast<float*>(smem) + kJoinThreads / 32 * D;
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sets = S::kRows / rows;   // CTAs of an item
@@ -751,7 +752,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
     if (shared) {
 #pragma unroll
       for (int c = 0; c < kCols; ++c) s_o[warp][kCols * lane + c] = v[c];
-      if (lane == 0) s_ml[warp] = make_float2(0.f, sum);
+      if (lane == 0) s_l[warp] = sum;
       __syncthreads();
       if (warp > 0) return;
       sum = 0.f;
@@ -759,7 +760,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
       for (int c = 0; c < kCols; ++c) v[c] = 0.f;
 #pragma unroll
       for (int w = 0; w < kJoinThreads / 32; ++w) {
-        sum += s_ml[w].y;
+        sum += s_l[w];
 #pragma unroll
         for (int c = 0; c < kCols; ++c) v[c] += s_o[w][kCols * lane + c];
       }
@@ -817,6 +818,7 @@ cudaError_t launch(KvAttentionArgs p, int sms, cudaStream_t st, int* launches) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * (S::kRows / rows)));
   cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = rows == 1 ? kJoinThreads / 32 * (D + 1) * sizeof(float) : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
