@@ -277,34 +277,37 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
       }
     }
   } else if (warp == 1) {
-    // ---------------------------------------------- MMA issuer (the leader's) ------
-    if (rank == 0) {
+    // ------------------------------- MMA issuer (one thread, the leader's) ---------
+    // The tensor pipe takes few MMAs ahead, so what this thread does between two of them
+    // shows: the next stage's barrier is tried between a stage's own MMAs, and descriptors are
+    // one addition. (A wait of the whole warp before each stage's MMAs: 836 cycles a stage
+    // where the MMAs need 512, with no stage ever late.)
+    if (rank == 0 && lane == 0) {
       int stage = 0, it = 0;
       uint32_t phase = 0;
       const uint32_t idesc = idesc_e4m3(BM, BN);
-      bool ok = true;
+      const uint64_t a_desc = smem_desc(smem_u32(sA), 16, 1024, 2), b_desc = smem_desc(smem_u32(sB), 16, 1024, 2);
+      bool ok = true, ready = false;
       for (int u = first; u < units && ok; u += step, ++it) {
         const int ab = it & 1;
         if (!mbar_wait_cluster(&acc_empty[ab], ((it >> 1) & 1) ^ 1, abort_flag, p.err)) break;
-        tc_fence_after();
         const uint32_t dacc = tmem + ab * BN;
         for (int kt = 0; kt < nk; ++kt) {
-          if (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
+          if (!ready && !mbar_wait(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t a0 = smem_u32(sA + stage * kHalf), b0 = smem_u32(sB + stage * kHalf);
-            const int nks = min(4, (p.K - kt * BK) / 32);   // K % 32 == 0: the last stage may hold fewer steps
-            for (int kk = 0; kk < nks; ++kk)
-              mma_f8<2>(dacc, smem_desc(a0 + 32 * kk, 16, 1024, 2), smem_desc(b0 + 32 * kk, 16, 1024, 2), idesc,
-                        (kt > 0 || kk > 0) ? 1u : 0u);
-            commit_pair(&empty[stage]);
-          }
-          __syncwarp();
+          const uint64_t ad = a_desc + static_cast<uint64_t>(stage * (kHalf / 16)), bd = b_desc + static_cast<uint64_t>(stage * (kHalf / 16));
+          uint64_t* const done = &empty[stage];
           if (++stage == kStages) { stage = 0; phase ^= 1; }
+          const int nks = min(4, (p.K - kt * BK) / 32);   // K % 32 == 0: the last stage may hold fewer steps
+          mma_f8<2>(dacc, ad, bd, idesc, kt > 0 ? 1u : 0u);
+          if (nks > 1) mma_f8<2>(dacc, ad + 2, bd + 2, idesc, 1u);
+          ready = mbar_try_wait(&full[stage], phase);
+          if (nks > 2) mma_f8<2>(dacc, ad + 4, bd + 4, idesc, 1u);
+          if (nks > 3) mma_f8<2>(dacc, ad + 6, bd + 6, idesc, 1u);
+          commit_pair(done);
         }
         if (!ok) break;
-        if (lane == 0) commit_pair(&acc_full[ab]);
-        __syncwarp();
+        commit_pair(&acc_full[ab]);
       }
     }
   } else {
@@ -423,23 +426,21 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
       }
     }
   } else if (warp == 1) {
-    bool ok = true;
-    for (int kt = k0; kt < k1; ++kt) {
-      const int i = kt - k0, stage = i % kStages;
-      if (!mbar_wait(&full[stage], (i / kStages) & 1, abort_flag, p.err)) { ok = false; break; }
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t a0 = smem_u32(smem + stage * kStage), b0 = a0 + kA;
+    if (lane == 0) {
+      const uint64_t desc = smem_desc(smem_u32(smem), 16, 1024, 2);
+      bool ok = true;
+      for (int kt = k0; kt < k1; ++kt) {
+        const int i = kt - k0, stage = i % kStages;
+        if (!mbar_wait(&full[stage], (i / kStages) & 1, abort_flag, p.err)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t ad = desc + static_cast<uint64_t>(stage * (kStage / 16)), bd = ad + kA / 16;
         const int nks = min(4, (p.K - kt * BK) / 32);
         for (int kk = 0; kk < nks; ++kk)
-          mma_f8<1>(tmem, smem_desc(a0 + 32 * kk, 16, 1024, 2), smem_desc(b0 + 32 * kk, 16, 1024, 2),
-                    idesc_e4m3(BM, BN), (i > 0 || kk > 0) ? 1u : 0u);
+          mma_f8<1>(tmem, ad + 2 * kk, bd + 2 * kk, idesc_e4m3(BM, BN), (i > 0 || kk > 0) ? 1u : 0u);
         tc_commit(&empty[stage]);
       }
-      __syncwarp();
+      if (ok) tc_commit(done);
     }
-    if (ok && lane == 0) tc_commit(done);
-    __syncwarp();
   }
   // every stage has been consumed when `done` completes: its memory takes the partial sums,
   // fp32 [token][128 weight rows]
