@@ -167,44 +167,55 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Eight outputs [n, n + 8) of token t from their sums; sx: the token's scale (times s_w where
-// that is one scale for all).
+// What eight columns [n, n + 8) share over the tokens: channel scales and bias.
+struct Columns {
+  float w[8], b[8];
+  __device__ __forceinline__ void load(const LinearFusedArgs& p, int n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] = 1.f;
+      b[i] = 0.f;
+    }
+    if (p.sw) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p.sw + n)), y = __ldg(reinterpret_cast<const float4*>(p.sw + n) + 1);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w; w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+    }
+    if (p.bias) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p.bias + n)), y = __ldg(reinterpret_cast<const float4*>(p.bias + n) + 1);
+      b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w; b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
+    }
+  }
+};
+
+// Those columns' outputs of token t, from their sums times the token's scale; r: their residual
+// (zeros without one, which add nothing but turn a -0 into +0).
 template <int kAct>
-__device__ __forceinline__ void finish8(const LinearFusedArgs& p, int64_t t, int n, const float (&acc)[8], float sx) {
-  float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (p.sw) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p.sw + n)), y = __ldg(reinterpret_cast<const float4*>(p.sw + n) + 1);
-    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w; w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
-  }
-  if (p.bias) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p.bias + n)), y = __ldg(reinterpret_cast<const float4*>(p.bias + n) + 1);
-    b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w; b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
-  }
-  uint4 r = make_uint4(0, 0, 0, 0);
-  if (p.residual) r = *reinterpret_cast<const uint4*>(p.residual + t * p.N + n);
+__device__ __forceinline__ void finish8(const LinearFusedArgs& p, int64_t t, int n, const float (&acc)[8],
+                                        const Columns& c, const uint4& r) {
   const uint32_t ru[4] = {r.x, r.y, r.z, r.w};
   uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo = activate<kAct>(fmaf(acc[2 * i], sx * w[2 * i], b[2 * i]));
-    float hi = activate<kAct>(fmaf(acc[2 * i + 1], sx * w[2 * i + 1], b[2 * i + 1]));
-    if (p.residual) {
-      lo += __uint_as_float(ru[i] << 16);
-      hi += __uint_as_float(ru[i] & 0xFFFF0000u);
-    }
-    o[i] = pack2(lo, hi);
-  }
+  for (int i = 0; i < 4; ++i)
+    o[i] = pack2(activate<kAct>(fmaf(acc[2 * i], c.w[2 * i], c.b[2 * i])) + __uint_as_float(ru[i] << 16),
+                 activate<kAct>(fmaf(acc[2 * i + 1], c.w[2 * i + 1], c.b[2 * i + 1])) + __uint_as_float(ru[i] & 0xFFFF0000u));
   *reinterpret_cast<uint4*>(p.out + t * p.N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ uint4 residual8(const LinearFusedArgs& p, int64_t t, int n) {
+  return p.residual ? *reinterpret_cast<const uint4*>(p.residual + t * p.N + n) : make_uint4(0, 0, 0, 0);
 }
 
 // ------------------------------------------------------------------------- pair ----
 namespace pair {
 constexpr int BM = 256, BN = 256;      // of the pair; each CTA loads half of either
-constexpr int kStages = 6;
-constexpr int kHalf = 128 * BK;        // 16 KB: a CTA's rows of one operand
+constexpr int kStages = 3;
+constexpr int kSub = 2;                // chunks of BK per stage: eight MMAs to a barrier and a commit
+constexpr int kHalf = 128 * BK;        // 16 KB: a CTA's rows of one operand, one chunk
+constexpr int kStage = 2 * kSub * kHalf;   // [chunk][x rows, weight rows]
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kSmemBytes = 1024 + kStages * 2 * kHalf + 256;
+constexpr int kTurn = 32 * 32 * 4;      // an epilogue warp's buffer: 32 tokens by 32 columns, fp32
+constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiWarps * kTurn + 256;
 }  // namespace pair
 
 template <int kAct>
@@ -214,9 +225,8 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
   using namespace pair;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = sA + kStages * kHalf;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + kStages * kHalf);   // the leader's: both CTAs' bytes
+  uint8_t* turn = smem + kStages * kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(turn + kEpiWarps * kTurn);   // the leader's: both CTAs' bytes
   uint64_t* empty = full + kStages;                                     // each CTA's
   uint64_t* acc_full = empty + kStages;                                 // each CTA's
   uint64_t* acc_empty = acc_full + 2;                                   // the leader's: both CTAs' epilogue warps
@@ -261,12 +271,16 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
       bool ok = true;
       for (int u = first; u < units && ok; u += step) {
         const int m0 = (u / n_tiles) * BM + 128 * static_cast<int>(rank), n0 = (u % n_tiles) * BN + 128 * static_cast<int>(rank);
-        for (int kt = 0; kt < nk; ++kt) {
+        for (int kt = 0; kt < nk; kt += kSub) {
           if (!mbar_wait_cluster(&empty[stage], phase ^ 1, abort_flag, p.err)) { ok = false; break; }
           const uint32_t bar = peer_addr(smem_u32(&full[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kHalf);
-          tma_load_2d_pair(sA + stage * kHalf, &tmap_x, bar, kt * BK, m0);
-          tma_load_2d_pair(sB + stage * kHalf, &tmap_w, bar, kt * BK, n0);
+          const int chunks = min(kSub, nk - kt);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kHalf * chunks);
+          for (int c = 0; c < chunks; ++c) {
+            uint8_t* dst = smem + stage * kStage + 2 * c * kHalf;
+            tma_load_2d_pair(dst, &tmap_x, bar, (kt + c) * BK, m0);
+            tma_load_2d_pair(dst + kHalf, &tmap_w, bar, (kt + c) * BK, n0);
+          }
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
       }
@@ -278,32 +292,35 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
     }
   } else if (warp == 1) {
     // ------------------------------- MMA issuer (one thread, the leader's) ---------
-    // The tensor pipe takes few MMAs ahead, so what this thread does between two of them
-    // shows: the next stage's barrier is tried between a stage's own MMAs, and descriptors are
-    // one addition. (A wait of the whole warp before each stage's MMAs: 836 cycles a stage
-    // where the MMAs need 512, with no stage ever late.)
+    // The tensor pipe takes few MMAs ahead, so this thread's own time shows: an MMA's issue
+    // about 92 cycles (the MMA runs 128), a commit about 200, a fence and a wait on a barrier that
+    // is complete about 80 each. Hence eight MMAs to a stage, the next stage's barrier tried
+    // between them, and descriptors that are one addition. (Per 128 of K, where the MMAs need
+    // 512 cycles: 836 with four MMAs to a stage and the warp waiting before each, 674 with the
+    // early try; no stage was ever late in either.)
     if (rank == 0 && lane == 0) {
       int stage = 0, it = 0;
       uint32_t phase = 0;
       const uint32_t idesc = idesc_e4m3(BM, BN);
-      const uint64_t a_desc = smem_desc(smem_u32(sA), 16, 1024, 2), b_desc = smem_desc(smem_u32(sB), 16, 1024, 2);
+      const uint64_t desc = smem_desc(smem_u32(smem), 16, 1024, 2);
       bool ok = true, ready = false;
       for (int u = first; u < units && ok; u += step, ++it) {
         const int ab = it & 1;
         if (!mbar_wait_cluster(&acc_empty[ab], ((it >> 1) & 1) ^ 1, abort_flag, p.err)) break;
         const uint32_t dacc = tmem + ab * BN;
-        for (int kt = 0; kt < nk; ++kt) {
+        for (int kt = 0; kt < nk; kt += kSub) {
           if (!ready && !mbar_wait(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t ad = a_desc + static_cast<uint64_t>(stage * (kHalf / 16)), bd = b_desc + static_cast<uint64_t>(stage * (kHalf / 16));
+          const uint64_t ad = desc + static_cast<uint64_t>(stage * (kStage / 16)), bd = ad + kHalf / 16;
           uint64_t* const done = &empty[stage];
           if (++stage == kStages) { stage = 0; phase ^= 1; }
-          const int nks = min(4, (p.K - kt * BK) / 32);   // K % 32 == 0: the last stage may hold fewer steps
-          mma_f8<2>(dacc, ad, bd, idesc, kt > 0 ? 1u : 0u);
-          if (nks > 1) mma_f8<2>(dacc, ad + 2, bd + 2, idesc, 1u);
-          ready = mbar_try_wait(&full[stage], phase);
-          if (nks > 2) mma_f8<2>(dacc, ad + 4, bd + 4, idesc, 1u);
-          if (nks > 3) mma_f8<2>(dacc, ad + 6, bd + 6, idesc, 1u);
+          const int steps = min(4 * kSub, (p.K - kt * BK) / 32);   // K % 32 == 0: the last stage may hold fewer
+#pragma unroll
+          for (int kk = 0; kk < 4 * kSub; ++kk) {
+            const int at = (kk / 4) * (2 * kHalf / 16) + 2 * (kk % 4);
+            if (kk < steps) mma_f8<2>(dacc, ad + at, bd + at, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+            if (kk == 4 * kSub - 3) ready = mbar_try_wait(&full[stage], phase);
+          }
           commit_pair(done);
         }
         if (!ok) break;
@@ -312,34 +329,50 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
     }
   } else {
     // --------------------------------------------------------------- epilogue -----
+    // Tensor memory gives a lane one token's columns; global memory wants a row's columns side by
+    // side. Each warp turns 32 x 32 sums through its own buffer (16-byte pieces permuted by
+    // the token, so that both sides are free of bank conflicts): then eight tokens' 64 bytes
+    // go out (and a residual's come in) per instruction instead of 32 tokens' 16. At 4096 x
+    // 2880 -> 5120 the direct stores paced the kernel: 60.1 us against 48.1 without them.
     const int q = warp & 3;              // tensor-memory lane quarter of this warp
     const int half = (warp - 2) >> 2;    // columns [128 half, 128 half + 128)
+    float4* const mine = reinterpret_cast<float4*>(turn + (warp - 2) * kTurn);
+    const int row = lane >> 2, col = 8 * (lane & 3);   // the lane's part of a pass: tokens row + 8 i, columns col ..
     int it = 0;
     for (int u = first; u < units; u += step, ++it) {
       const int ab = it & 1;
-      const int64_t t = static_cast<int64_t>(u / n_tiles) * BM + 128 * rank + 32 * q + lane;
+      const int64_t t0 = static_cast<int64_t>(u / n_tiles) * BM + 128 * rank + 32 * q;
       const int n0 = (u % n_tiles) * BN;
-      const float sx = t < p.T ? (p.sx ? __ldg(p.sx + t) * p.s : p.s) : 0.f;
+      const float sx = t0 + lane < p.T ? (p.sx ? __ldg(p.sx + t0 + lane) * p.s : p.s) : 0.f;
       if (!mbar_wait_cluster(&acc_full[ab], (it >> 1) & 1, abort_flag, p.err)) break;
       __syncwarp();
       tc_fence_after();
       const uint32_t tbase = tmem + ab * BN + (static_cast<uint32_t>(32 * q) << 16);
       for (int c0 = 128 * half; c0 < 128 * half + 128; c0 += 32) {
-        if (n0 + c0 >= p.N) break;
+        if (n0 + c0 >= p.N || t0 >= p.T) break;
         uint32_t v[32];
         tc_ld_32x32b_x32(tbase + c0, v);
-        if (t < p.T) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = n0 + c0 + 8 * j;
-            if (n < p.N) {   // N % 8 == 0: a group of 8 columns is wholly in or out
-              float a[8];
+        for (int j = 0; j < 8; ++j)
+          mine[8 * lane + (j ^ (lane & 7))] =
+              make_float4(__uint_as_float(v[4 * j]) * sx, __uint_as_float(v[4 * j + 1]) * sx,
+                          __uint_as_float(v[4 * j + 2]) * sx, __uint_as_float(v[4 * j + 3]) * sx);
+        __syncwarp();
+        const int n = n0 + c0 + col;
+        if (n < p.N) {   // N % 8 == 0: a group of 8 columns is wholly in or out
+          Columns c;
+          c.load(p, n);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) a[i] = __uint_as_float(v[8 * j + i]);
-              finish8<kAct>(p, t, n, a, sx);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int r = row + 8 * i;
+            if (t0 + r >= p.T) break;
+            const uint4 res = residual8(p, t0 + r, n);
+            const float4 x = mine[8 * r + ((col / 4) ^ (r & 7))], y = mine[8 * r + ((col / 4 + 1) ^ (r & 7))];
+            const float a[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            finish8<kAct>(p, t0 + r, n, a, c, res);
           }
         }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -480,7 +513,12 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
       a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
     }
     const int64_t t = t0 + tok;
-    finish8<kAct>(p, t, n, a, p.sx ? __ldg(p.sx + t) * p.s : p.s);
+    const float sx = p.sx ? __ldg(p.sx + t) * p.s : p.s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] *= sx;
+    Columns c;
+    c.load(p, n);
+    finish8<kAct>(p, t, n, a, c, residual8(p, t, n));
   }
   __syncwarp();
   cluster_sync();      // this CTA's sums have been read
