@@ -1230,7 +1230,7 @@ int mxfp4_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t l
   if (int rc = current_device_ws(&ws)) return rc;
   const mxmoe::KvAppendArgs a{k, v, ldk, ldv, slots, num_pages << shift, T, Hkv, D, shift,
                               k_blocks, k_scales, v_blocks, v_scales, ws->err};
-  cudaError_t e = mxmoe::launch_kv_append(a, static_cast<cudaStream_t>(stream));
+  cudaError_t e = mxmoe::launch_kv_append(a, ws->sms, static_cast<cudaStream_t>(stream));
   if (e) return cuda_fail(e, "kv append launch");
   t_last_launches = 1;
   return MXMOE_OK;

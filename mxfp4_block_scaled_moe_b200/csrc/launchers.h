@@ -247,7 +247,7 @@ struct KvAppendArgs {
   uint8_t* v_scales;
   int* err;
 };
-cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
+cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t st);
 
 // attention over that cache (csrc/kv_attention.cu): D 64 or 128. launch_kv_attention sets RT,
 // whole and the workspace pointers.
