@@ -8,6 +8,7 @@ bf16 tensors are passed as their bit patterns (torch.bfloat16 storage).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -131,6 +132,8 @@ def mxfp4_quantize(w: torch.Tensor, blocks=None, scales=None, stream=None):
 def mxfp4_dequantize(blocks: torch.Tensor, scales: torch.Tensor, out_dtype=torch.float32,
                      out=None, stream=None):
     """(..., K/2) uint8 + (..., K/32) uint8 -> (..., K) fp32 or bf16."""
+    if stream is None and (out_dtype is torch.bfloat16 or out_dtype is torch.float32):
+        return (_ops or _host_ops()).dequantize(blocks, scales, out, out_dtype is torch.float32)
     _dev(blocks, torch.uint8, "blocks")
     _dev(scales, torch.uint8, "scales")
     K = blocks.shape[-1] * 2
@@ -363,101 +366,32 @@ def moe_combine(y, topk_idx, topk_w, inv, out=None, stream=None):
 
 # -------------------------------------------------------------- attention half -----
 
-# These operators take a few microseconds on the GPU, so their host side is kept short: flat
-# checks whose messages are formed only on failure, no checks of tensors made here, raw
-# device and stream handles.
+# These operators take a few microseconds on the GPU, so their host side (checks of the tensors,
+# outputs, the C ABI call) is native: csrc/host_ops.cpp. An operator given `stream` runs with
+# that stream current, so that the outputs and workspaces it makes belong to the stream
+# that uses them; otherwise it is the current stream of the tensors' device.
 
-def _device(t, name):
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
+_ops = None
 
 
-def _refuse(t, dtype, shape, dev, name):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the other tensors on cuda:{dev}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
+def _host_ops():
+    """Load the extension (once) and hand it the library's entry points."""
+    global _ops
+    if _ops is None:
+        L = lib()
+        path = os.path.join(_HERE, "_host_ops.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: run mxfp4_block_scaled_moe_b200/build.py")
+        spec = importlib.util.spec_from_file_location("_host_ops", path)
+        ops = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ops)
 
+        def fail(rc, name):
+            raise MxmoeError(rc, name, L.mxmoe_last_error().decode(errors="replace"))
 
-def _arg(t, dtype, shape, dev, name):
-    """Device pointer of a dense tensor of that type, shape and device (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-        _refuse(t, dtype, shape, dev, name)
-    return t.data_ptr()
-
-
-def _rows(t, H, dev, name):
-    """(device pointer, row stride) of a bf16 tensor (..., H) as rows: a dense tensor of any
-    rank, or two-dimensional rows cut from wider ones."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
-        _refuse(t, torch.bfloat16, None, dev, name)
-    if t.is_contiguous():
-        return t.data_ptr(), H
-    if t.dim() != 2 or t.stride(1) != 1:
-        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
-    return t.data_ptr(), t.stride(0)
-
-
-def _run_on(dev, name, *args):
-    """_call with the tensors' device current; that device's current stream goes last. (An
-    operator given `stream` calls itself with that stream current first, so that the
-    outputs and workspaces it makes belong to the stream that uses them.)"""
-    if dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
-            return _run_on(dev, name, *args)
-    L = _lib or lib()
-    rc = getattr(L, name)(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if rc != OK:
-        raise MxmoeError(rc, name, L.mxmoe_last_error().decode(errors="replace"))
-
-
-def _norm(x, weight, residual, eps, sum_out, y, q, fp8, act_scale):
-    """Shared by the two norms: makes the outputs that were not given, checks the rest."""
-    dev = _device(x, "x")
-    shape = x.shape
-    H = shape[-1]
-    px, ldx = _rows(x, H, dev, "x")
-    pr = ps = py = pq = pt = s = scale = None
-    ldr = H
-    if residual is not None:
-        if residual.shape != shape:
-            raise ValueError(f"residual must have x's shape {tuple(shape)}, got {tuple(residual.shape)}")
-        pr, ldr = _rows(residual, H, dev, "residual")
-        if sum_out is None:
-            sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
-            ps = sum_out.data_ptr()
-        else:
-            ps = _arg(sum_out, torch.bfloat16, shape, dev, "sum_out")
-    elif sum_out is not None:
-        raise ValueError("sum_out goes with a residual")
-    if y is not None:
-        py = _arg(y, torch.bfloat16, shape, dev, "y")
-    elif not fp8:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
-        py = y.data_ptr()
-    if fp8:
-        if q is None:
-            q = torch.empty_like(x, dtype=torch.uint8, memory_format=torch.contiguous_format)
-            pq = q.data_ptr()
-        else:
-            pq = _arg(q, torch.uint8, shape, dev, "q")
-        if act_scale is None:
-            scale = x.new_empty(shape[:-1], dtype=torch.float32)
-            pt = scale.data_ptr()
-        else:
-            s = ctypes.byref(_f32(act_scale))
-    _run_on(dev, "rmsnorm_residual", px, ldx, pr, ldr, _arg(weight, torch.bfloat16, (H,), dev, "weight"), eps,
-            x.numel() // H if H else 0, H, ps, py, pq, pt, s)
-    return y, q, scale, sum_out
+        ops.setup(fail, {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _SIGS})
+        _ops = ops
+    return _ops
 
 
 def rmsnorm_residual(x, weight, residual=None, eps=1e-5, sum_out=None, y=None, stream=None):
@@ -467,7 +401,7 @@ def rmsnorm_residual(x, weight, residual=None, eps=1e-5, sum_out=None, y=None, s
     if stream is not None:
         with torch.cuda.stream(stream):
             return rmsnorm_residual(x, weight, residual, eps, sum_out, y)
-    y, _, _, sum_out = _norm(x, weight, residual, eps, sum_out, y, None, False, None)
+    y, _, _, sum_out = (_ops or _host_ops()).norm(x, weight, residual, eps, None, sum_out, None, y, False)
     return y, sum_out
 
 
@@ -479,7 +413,7 @@ def rmsnorm_residual_fp8(x, weight, residual=None, eps=1e-5, act_scale=None, sum
     if stream is not None:
         with torch.cuda.stream(stream):
             return rmsnorm_residual_fp8(x, weight, residual, eps, act_scale, sum_out, q, y)
-    return _norm(x, weight, residual, eps, sum_out, y, q, True, act_scale)[1:]
+    return (_ops or _host_ops()).norm(x, weight, residual, eps, act_scale, sum_out, q, y, True)[1:]
 
 
 ACTS = {None: 0, "silu": 1, "gelu": 2}
@@ -493,63 +427,9 @@ def fp8_linear_fused(xq, wq, s_x, s_w, bias=None, act=None, residual=None, out=N
     if stream is not None:
         with torch.cuda.stream(stream):
             return fp8_linear_fused(xq, wq, s_x, s_w, bias, act, residual, out)
-    dev = _device(xq, "xq")
-    T, K = xq.shape
-    N = wq.shape[0]
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}, got {act!r}")
-    px = pw = None
-    if isinstance(s_x, torch.Tensor):
-        px, s_x = _arg(s_x, torch.float32, (T,), dev, "s_x"), 1.0
-    if isinstance(s_w, torch.Tensor):
-        pw, s_w = _arg(s_w, torch.float32, (N,), dev, "s_w"), 1.0
-    if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=xq.device)
-        po = out.data_ptr()
-    else:
-        po = _arg(out, torch.bfloat16, (T, N), dev, "out")
-    _run_on(dev, "fp8_linear_fused", _arg(xq, torch.uint8, (T, K), dev, "xq"), T, K,
-            _arg(wq, torch.uint8, (N, K), dev, "wq"), N, px, s_x, pw, s_w, _arg(bias, torch.float32, (N,), dev, "bias"),
-            ACTS[act], _arg(residual, torch.bfloat16, (T, N), dev, "residual"), po)
-    return out
-
-
-def _cache(k_blocks, k_scales, v_blocks, v_scales, dev):
-    """(pointers, num_pages, Hkv, page_size, D) of a paged cache's four arrays."""
-    shape = k_blocks.shape
-    if len(shape) != 4:
-        raise ValueError(f"k_blocks must be (num_pages, Hkv, page_size, D/2), got {tuple(shape)}")
-    pages, Hkv, page_size, half = shape
-    sc = (pages, Hkv, page_size, half // 16)
-    ptrs = (_arg(k_blocks, torch.uint8, shape, dev, "k_blocks"), _arg(k_scales, torch.uint8, sc, dev, "k_scales"),
-            _arg(v_blocks, torch.uint8, shape, dev, "v_blocks"), _arg(v_scales, torch.uint8, sc, dev, "v_scales"))
-    return ptrs, pages, Hkv, page_size, 2 * half
-
-
-def _tokens(t, dev, name):
-    """(device pointer, token stride) of a bf16 tensor (..., heads, D) whose heads are dense and
-    whose tokens are one stride apart."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
-        _refuse(t, torch.bfloat16, None, dev, name)
-    shape = t.shape
-    if t.is_contiguous():
-        return t.data_ptr(), shape[-2] * shape[-1]
-    stride = t.stride()
-    if stride[-1] != 1 or stride[-2] != shape[-1]:
-        raise ValueError(f"{name}: each token's heads must be dense")
-    if len(shape) == 3 and shape[0] > 1:
-        return t.data_ptr(), stride[0]
-    step = n = None
-    for size, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
-        if size == 1:
-            continue
-        if step is None:
-            step, n = st, size
-        elif st != step * n:
-            raise ValueError(f"{name}: the tokens must be one stride apart")
-        else:
-            n *= size
-    return t.data_ptr(), shape[-2] * shape[-1] if step is None else step
+    return (_ops or _host_ops()).linear(xq, wq, s_x, s_w, bias, ACTS[act], residual, out)
 
 
 def mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales, stream=None):
@@ -560,31 +440,15 @@ def mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales, stream=
     if stream is not None:
         with torch.cuda.stream(stream):
             return mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales)
-    dev = _device(k, "k")
-    ptrs, pages, Hkv, page_size, D = _cache(k_blocks, k_scales, v_blocks, v_scales, dev)
-    T = k.shape[0]
-    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
-        raise ValueError(f"k and v must be (T, {Hkv}, {D}), got {tuple(k.shape)} and {tuple(v.shape)}")
-    pk, ldk = _tokens(k, dev, "k")
-    pv, ldv = _tokens(v, dev, "v")
-    _run_on(dev, "mxfp4_kv_append", pk, ldk, pv, ldv, _arg(slots, torch.int64, (T,), dev, "slots"), T, Hkv, D, *ptrs,
-            pages, page_size)
-
-
-_attention_bytes: dict = {}
+    (_ops or _host_ops()).append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales)
 
 
 def mxfp4_kv_attention_workspace(B, Lq, Hq, Hkv, D, device=None) -> int:
     """Bytes of workspace that mxfp4_kv_attention needs for these sizes."""
-    dev = torch.device("cuda" if device is None else device).index
-    dev = torch.cuda.current_device() if dev is None else dev
-    key = (dev, B, Lq, Hq, Hkv, D)
-    if key not in _attention_bytes:
-        n = ctypes.c_int64(0)
-        with torch.cuda.device(dev):
-            _call("mxfp4_kv_attention_workspace", B, Lq, Hq, Hkv, D, ctypes.byref(n))
-        _attention_bytes[key] = n.value
-    return _attention_bytes[key]
+    n = ctypes.c_int64(0)
+    with torch.cuda.device(device):
+        _call("mxfp4_kv_attention_workspace", B, Lq, Hq, Hkv, D, ctypes.byref(n))
+    return n.value
 
 
 def mxfp4_kv_attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, seq_lens, scale=None, window=0, sinks=None,
@@ -599,35 +463,8 @@ def mxfp4_kv_attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, s
         with torch.cuda.stream(stream):
             return mxfp4_kv_attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, seq_lens, scale, window,
                                       sinks, out, workspace)
-    dev = _device(q, "q")
-    ptrs, pages, Hkv, page_size, D = _cache(k_blocks, k_scales, v_blocks, v_scales, dev)
-    shape = q.shape
-    if len(shape) not in (3, 4) or shape[-1] != D:
-        raise ValueError(f"q must be (B, Lq, Hq, {D}) or (B, Hq, {D}), got {tuple(shape)}")
-    B, Hq = shape[0], shape[-2]
-    Lq = shape[1] if len(shape) == 4 else 1
-    pq, ldq = _tokens(q, dev, "q")
-    if block_table.dim() != 2:
-        raise ValueError(f"block_table must be (B, max_pages), got {tuple(block_table.shape)}")
-    max_pages = block_table.shape[1]
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        po = out.data_ptr()
-    else:
-        po = _arg(out, torch.bfloat16, shape, dev, "out")
-    if workspace is None:
-        nbytes = _attention_bytes.get((dev, B, Lq, Hq, Hkv, D))
-        if nbytes is None:
-            nbytes = mxfp4_kv_attention_workspace(B, Lq, Hq, Hkv, D, q.device)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        pw = workspace.data_ptr()
-    else:
-        nbytes, pw = workspace.numel(), _arg(workspace, torch.uint8, workspace.shape, dev, "workspace")
-    _run_on(dev, "mxfp4_kv_attention", pq, ldq, *ptrs, pages, page_size,
-            _arg(block_table, torch.int32, (B, max_pages), dev, "block_table"), max_pages,
-            _arg(seq_lens, torch.int32, (B,), dev, "seq_lens"), _arg(sinks, torch.float32, (Hq,), dev, "sinks"), B, Lq,
-            Hq, Hkv, D, D ** -0.5 if scale is None else scale, window, po, pw, nbytes)
-    return out
+    return (_ops or _host_ops()).attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, seq_lens, scale, window,
+                                           sinks, out, workspace)
 
 
 def mxmoe_check(stream=None):

@@ -4,6 +4,9 @@ Every .cu file under csrc/ is compiled by nvcc with
 ``-gencode arch=compute_100a,code=sm_100a -O3 -lineinfo`` (no fast-math: IEEE division
 and square roots, no flush-to-zero) and linked into one shared library with the CUDA
 runtime linked statically. The library lands next to this file, inside the package.
+
+csrc/host_ops.cpp, the operators' native host side, becomes the Python extension
+_host_ops.so beside it (compiled by g++ against the installed torch).
 """
 from __future__ import annotations
 
@@ -12,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "mxfp4moe")
 LIB = os.path.join(HERE, "libmxfp4moe.so")
+HOST_OPS = os.path.join(HERE, "_host_ops.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
               "-Xptxas", "-warn-spills", "-I", INCLUDE, "-I", CSRC]
@@ -42,11 +47,32 @@ def _stale(lib, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_host_ops(force: bool = False) -> str:
+    src = os.path.join(CSRC, "host_ops.cpp")
+    if not force and not _stale(HOST_OPS, [src, os.path.join(INCLUDE, "mxfp4_moe.h"), __file__]):
+        return HOST_OPS
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = cpp_extension.include_paths() + [os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = f"{HOST_OPS}.{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[a for i in inc for a in ("-isystem", i)],
+           src, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST_OPS)
+    return HOST_OPS
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     srcs = sources()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     headers.append(os.path.join(INCLUDE, "mxfp4_moe.h"))
     if not force and not _stale(LIB, srcs + headers + [__file__]):
+        build_host_ops()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -62,7 +88,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
+        host = ex.submit(build_host_ops, force)
         objs = list(ex.map(compile_one, srcs))
+        host.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs, "-lpthread", "-ldl", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
