@@ -338,18 +338,32 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
     const int half = (warp - 2) >> 2;    // columns [128 half, 128 half + 128)
     float4* const mine = reinterpret_cast<float4*>(turn + (warp - 2) * kTurn);
     const int row = lane >> 2, col = 8 * (lane & 3);   // the lane's part of a pass: tokens row + 8 i, columns col ..
+    // a 32-column chunk's residual, fetched a chunk ahead (from HBM; the column constants, which
+    // every token tile reads again, come from L1 or L2)
+    const auto fetch = [&](uint4 (&res)[4], int64_t t0, int n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)   // N % 8 == 0: a group of 8 columns is wholly in or out
+        res[i] = n < p.N && t0 + row + 8 * i < p.T ? residual8(p, t0 + row + 8 * i, n) : make_uint4(0, 0, 0, 0);
+    };
     int it = 0;
     for (int u = first; u < units; u += step, ++it) {
       const int ab = it & 1;
       const int64_t t0 = static_cast<int64_t>(u / n_tiles) * BM + 128 * rank + 32 * q;
-      const int n0 = (u % n_tiles) * BN;
+      const int n0 = (u % n_tiles) * BN + 128 * half;
       const float sx = t0 + lane < p.T ? (p.sx ? __ldg(p.sx + t0 + lane) * p.s : p.s) : 0.f;
+      uint4 res[4], ahead[4];
+      fetch(res, t0, n0 + col);
       if (!mbar_wait_cluster(&acc_full[ab], (it >> 1) & 1, abort_flag, p.err)) break;
       __syncwarp();
       tc_fence_after();
-      const uint32_t tbase = tmem + ab * BN + (static_cast<uint32_t>(32 * q) << 16);
-      for (int c0 = 128 * half; c0 < 128 * half + 128; c0 += 32) {
+      const uint32_t tbase = tmem + ab * BN + 128 * half + (static_cast<uint32_t>(32 * q) << 16);
+#pragma unroll
+      for (int c0 = 0; c0 < 128; c0 += 32) {
         if (n0 + c0 >= p.N || t0 >= p.T) break;
+        const int n = n0 + c0 + col;
+        Columns cols;
+        if (n < p.N) cols.load(p, n);
+        if (c0 < 96) fetch(ahead, t0, n + 32);
         uint32_t v[32];
         tc_ld_32x32b_x32(tbase + c0, v);
 #pragma unroll
@@ -358,21 +372,16 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
               make_float4(__uint_as_float(v[4 * j]) * sx, __uint_as_float(v[4 * j + 1]) * sx,
                           __uint_as_float(v[4 * j + 2]) * sx, __uint_as_float(v[4 * j + 3]) * sx);
         __syncwarp();
-        const int n = n0 + c0 + col;
-        if (n < p.N) {   // N % 8 == 0: a group of 8 columns is wholly in or out
-          Columns c;
-          c.load(p, n);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = row + 8 * i;
-            if (t0 + r >= p.T) break;
-            const uint4 res = residual8(p, t0 + r, n);
-            const float4 x = mine[8 * r + ((col / 4) ^ (r & 7))], y = mine[8 * r + ((col / 4 + 1) ^ (r & 7))];
-            const float a[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            finish8<kAct>(p, t0 + r, n, a, c, res);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int r = row + 8 * i;
+          const float4 x = mine[8 * r + ((col / 4) ^ (r & 7))], y = mine[8 * r + ((col / 4 + 1) ^ (r & 7))];
+          const float a[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          if (n < p.N && t0 + r < p.T) finish8<kAct>(p, t0 + r, n, a, cols, res[i]);
         }
         __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) res[i] = ahead[i];
       }
       tc_fence_before();
       __syncwarp();
@@ -475,6 +484,22 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
       if (ok) tc_commit(done);
     }
   }
+  // the cluster's CTAs share the tile's (token, 8 rows) groups; what this thread's first one
+  // needs from global memory is fetched while the products run
+  const int tokens = min(BN, p.T - t0), groups = tokens * (BM / 8);
+  const int g0 = rank * kThreads + threadIdx.x;
+  Columns cols;
+  uint4 res = make_uint4(0, 0, 0, 0);
+  float sx = 0.f;
+  const auto fetch = [&](int gi) {
+    const int n = m0 + 8 * (gi % (BM / 8));
+    const int64_t t = t0 + gi / (BM / 8);
+    if (gi >= groups || n >= p.N) return;
+    cols.load(p, n);
+    res = residual8(p, t, n);
+    sx = p.sx ? __ldg(p.sx + t) * p.s : p.s;
+  };
+  fetch(g0);
   // every stage has been consumed when `done` completes: its memory takes the partial sums,
   // fp32 [token][128 weight rows]
   float* sums = reinterpret_cast<float*>(smem);
@@ -499,26 +524,21 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
   }
   __syncwarp();
   cluster_sync();
-  // the cluster's CTAs share the tile's (token, 8 rows) groups; sums in rank order
-  const int tokens = min(BN, p.T - t0), groups = tokens * (BM / 8);
   const uint32_t base = smem_u32(sums);
-  for (int gi = rank * kThreads + threadIdx.x; gi < groups; gi += ks * kThreads) {
+  for (int gi = g0; gi < groups; gi += ks * kThreads) {
     const int tok = gi / (BM / 8), n = m0 + 8 * (gi % (BM / 8));
+    if (gi != g0) fetch(gi);
     if (n >= p.N) continue;
     float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int r = 0; r < ks; ++r) {
+    for (int r = 0; r < ks; ++r) {   // in rank order
       const uint32_t at = peer_addr(base + 4 * (tok * BM + 8 * (gi % (BM / 8))), r);
       const float4 x = ld_peer(at), y = ld_peer(at + 16);
       a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
       a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
     }
-    const int64_t t = t0 + tok;
-    const float sx = p.sx ? __ldg(p.sx + t) * p.s : p.s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] *= sx;
-    Columns c;
-    c.load(p, n);
-    finish8<kAct>(p, t, n, a, c, residual8(p, t, n));
+    finish8<kAct>(p, t0 + tok, n, a, cols, res);
   }
   __syncwarp();
   cluster_sync();      // this CTA's sums have been read
@@ -558,7 +578,7 @@ cudaError_t launch_pair(const LinearFusedArgs& p, int sms, cudaStream_t st) {
 // GPC, so a size that does not divide a GPC's SMs leaves some idle (the activations' kernels
 // are alike in registers and shared memory). Asked once per device, tile and size.
 template <int BN>
-int clusters_at_once(int ks, cudaLaunchConfig_t cfg) {
+int clusters_at_once(int ks, const cudaLaunchConfig_t& cfg) {
   static std::atomic<int> known[64][linf::split::kMaxK + 1];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
@@ -574,6 +594,27 @@ int clusters_at_once(int ks, cudaLaunchConfig_t cfg) {
   return n;
 }
 
+// K ranges of the split kernel: the most whose clusters all run at once.
+template <int BN>
+int split_ranges(int64_t tiles, int K, int sms) {
+  using namespace linf;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(split::kThreads);
+  cfg.dynamicSmemBytes = split::smem_bytes(BN);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int ks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({split::kMaxK, cdiv(K, BK), sms / tiles})));
+  for (; ks > 1; --ks) {
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
+    cfg.gridDim = dim3(static_cast<unsigned>(ks));
+    if (tiles <= clusters_at_once<BN>(ks, cfg)) break;
+  }
+  return ks;
+}
+
 template <int BN, int kAct>
 cudaError_t launch_split(const LinearFusedArgs& p, int sms, cudaStream_t st) {
   using namespace linf;
@@ -584,35 +625,40 @@ cudaError_t launch_split(const LinearFusedArgs& p, int sms, cudaStream_t st) {
   cudaError_t e = limit.raise(fp8_linear_split_kernel<BN, kAct>, smem);
   if (e != cudaSuccess) return e;
   const int m_tiles = static_cast<int>(cdiv(p.N, split::BM)), t_tiles = static_cast<int>(cdiv(p.T, BN));
-  const int nk = static_cast<int>(cdiv(p.K, BK));
+  const int ks = split_ranges<BN>(static_cast<int64_t>(m_tiles) * t_tiles, p.K, sms);
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(m_tiles * ks), static_cast<unsigned>(t_tiles));
   cfg.blockDim = dim3(split::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // the most K ranges whose clusters all run at once
-  int ks = std::max(1, std::min({split::kMaxK, nk, sms / (m_tiles * t_tiles)}));
-  for (; ks > 1; --ks) {
-    attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
-    cfg.gridDim = dim3(static_cast<unsigned>(m_tiles * ks), static_cast<unsigned>(t_tiles));
-    if (m_tiles * t_tiles <= clusters_at_once<BN>(ks, cfg)) break;
-  }
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
-  cfg.gridDim = dim3(static_cast<unsigned>(m_tiles * ks), static_cast<unsigned>(t_tiles));
   return cudaLaunchKernelEx(&cfg, fp8_linear_split_kernel<BN, kAct>, mw, mx, p, ks);
+}
+
+// Which kernel for more than 128 tokens: the shorter by what each measured on a B200 over 22 sizes,
+// in units of 10 ns with nk = ceil(K / 128): a round of pairs 1000 + 29 nk (the first; 29 nk each
+// further one), a wave of split CTAs 800 + 42 nk / ks. E.g. 512 x 2880 -> 5120: pairs 19.7 us,
+// split 37.1; 512 x 4096 -> 640: 19.3, 15.0; 200 x 2880 -> 5120: 16.9, 18.6; 200 x 1024 -> 8192: 13.1,
+// 12.4; 4000 x 8192 -> 256: 30.8, 23.8.
+bool pairs_are_shorter(const LinearFusedArgs& p, int sms) {
+  using namespace linf;
+  const int64_t nk = cdiv(p.K, BK);
+  const int64_t rounds = cdiv(cdiv(p.T, pair::BM) * cdiv(p.N, pair::BN), std::max(1, sms / 2));
+  const int64_t tiles = cdiv(p.N, split::BM) * cdiv(p.T, 128);
+  const int ks = split_ranges<128>(tiles, p.K, sms);
+  const int64_t waves = cdiv(tiles * ks, sms);
+  return 1000 + 29 * nk * rounds < waves * (800 + 42 * nk / ks);
 }
 
 template <int kAct>
 cudaError_t launch_act(const LinearFusedArgs& p, int sms, cudaStream_t st) {
-  using namespace linf;
-  const int64_t pairs = cdiv(p.T, pair::BM) * cdiv(p.N, pair::BN);
-  if (p.T > 128 && 3 * pairs >= sms) return launch_pair<kAct>(p, sms, st);
+  if (p.T > 128 && pairs_are_shorter(p, sms)) return launch_pair<kAct>(p, sms, st);
   if (p.T <= 16) return launch_split<16, kAct>(p, sms, st);
   if (p.T <= 32) return launch_split<32, kAct>(p, sms, st);
   if (p.T <= 64) return launch_split<64, kAct>(p, sms, st);
