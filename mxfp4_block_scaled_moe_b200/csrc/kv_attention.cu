@@ -35,17 +35,22 @@
 namespace mxmoe {
 namespace kva {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kJoinThreads = 256;
 
-// A unit is 64 keys of 64 values for 8 rows, else 32 keys: what the accumulators of a
-// step leave room for in 128 registers.
-constexpr int unit_keys(int D, int nt) { return D == 64 && nt == 1 ? 64 : 32; }
+// A unit is 64 keys of 64 values or 32 of 128, 4 KB of codes: what a step's products, scores and
+// weights leave room for in registers. (32 keys of 64 values: 16 rows 47.8 us against 45.2.)
+constexpr int unit_keys(int D) { return D == 64 ? 64 : 32; }
+
+// One CTA per SM. Twelve warps leave each 168 registers; sixteen (two CTAs, 128 registers) spilled or
+// held fewer products in flight: 32 sequences of up to 4096 keys, 8 heads of 64 for 64: 32.3 us
+// against 30.8; 8 heads of 128 for 32: 43.6 against 40.9. 16 rows of 128 columns need more: eight
+// warps 65.3 us, twelve 73.1.
+constexpr int warps(int D, int nt) { return D == 128 && nt == 2 ? 8 : 12; }
 
 template <int D, int NT>
 struct Shape {
-  static constexpr int kUnit = unit_keys(D, NT);
+  static constexpr int kWarps = warps(D, NT), kThreads = 32 * kWarps;
+  static constexpr int kUnit = unit_keys(D);
   static constexpr int kTiles = kUnit / 16;
   static constexpr int kRows = 8 * NT;
   static constexpr int kBlocks = D / 32;               // MXFP4 blocks of a row
@@ -56,7 +61,6 @@ struct Shape {
   static constexpr int kStages = 3;
   static constexpr int kFactors = 2 * kBlocks * kUnit * 4;   // a unit's scales as fp32, keys' and values'
   static constexpr int kSmem = kWarps * (kStages * kStageBytes + kFactors);
-  static constexpr int kCtas = D == 64 || NT == 1 ? 2 : 1;   // per SM, by registers
 };
 
 // ------------------------------------------------------------------ small pieces ---
@@ -200,7 +204,12 @@ struct Cursor {
     end = start + max(1, (len - first + kUnit - 1) / kUnit);
     key0 = first - kUnit * start;
   }
-  __device__ int key(int unit) const { return key0 + kUnit * unit; }
+  // one item shared by `ways` warps: this one takes every ways-th unit from `way` on
+  __device__ void share(int way, int ways) {
+    end = (end - way + ways - 1) / ways;   // 0 for a way past the last unit (end + ways - 1 - way >= 0)
+    key0 += kUnit * way;
+  }
+  __device__ int key(const KvAttentionArgs& p, int unit) const { return key0 + p.unit_step * unit; }
   __device__ void next(const KvAttentionArgs& p) {
     if (++rt == p.RT) {
       rt = 0;
@@ -214,8 +223,9 @@ struct Cursor {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_kernel(const KvAttentionArgs p) {
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel(const KvAttentionArgs p) {
   using S = Shape<D, NT>;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_sum[kWarps];
   __shared__ int s_pre[kThreads];
@@ -230,17 +240,25 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
   int count = 0, start = 0;   // start: of the run's first item, in the run
   Cursor<S::kUnit> cur;
   cur.b = -1;
-  if (p.whole) {
+  if (p.whole > 1) {   // at most one item for each group of so many warps
+    const int ways = p.whole, way = warp % ways, item = warp / ways * gridDim.x + blockIdx.x;
+    if (item >= p.B * per_seq) return;
+    cur.b = item / per_seq;
+    cur.h = item % per_seq / p.RT;
+    cur.rt = item % p.RT;
+    cur.open(p, 0);
+    cur.share(way, ways);
+    count = cur.end;
+  } else if (p.whole) {
     const int items = p.B * per_seq, each = (items + runs - 1) / runs;
     const int i0 = run * each, i1 = min(items, i0 + each);
     for (int i = i0 + lane; i < i1; i += 32) count += units_of<S::kUnit>(p, seq_len(p, i / per_seq));
     count = __reduce_add_sync(0xffffffffu, count);
-    if (count > 0) {
-      cur.b = i0 / per_seq;
-      cur.h = i0 % per_seq / p.RT;
-      cur.rt = i0 % p.RT;
-      cur.open(p, 0);
-    }
+    if (count == 0) return;
+    cur.b = i0 / per_seq;
+    cur.h = i0 % per_seq / p.RT;
+    cur.rt = i0 % p.RT;
+    cur.open(p, 0);
   } else {
     // pass 0 counts the line's units, pass 1 finds the run's first; a batch of one chunk of
     // kThreads sequences needs its prefix sums once
@@ -294,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
     }
     if (threadIdx.x == 0) s_per = per;
     __syncthreads();
+    if (count == 0) return;
   }
-  if (count == 0) return;
 
   // ---- this warp's ring of units ----
   uint8_t* const ring = smem + warp * (S::kStages * S::kStageBytes + S::kFactors);
@@ -319,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
   auto look = [&]() {
     if (in_unit >= count) return;
     if (in_unit >= in.end) in.next(p);
-    const int key = in.key(in_unit) + 16 * lane;
+    const int key = in.key(p, in_unit) + 16 * lane;
     // keys that no query sees need no page
     in_need = lane < S::kTiles && key < in.len && key + 16 > first_seen(p, in.len);
     if (in_need) pid = __ldg(p.block_table + static_cast<int64_t>(in.b) * p.max_pages + (key >> p.page_shift));
@@ -330,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
       const bool ok = in_need && static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.num_pages);
       if (in_need && !ok) set_device_error(p.err, MXMOE_EDEVICE);   // a page outside the cache
       unsigned pages = __ballot_sync(0xffffffffu, ok);
-      const int key = in.key(in_unit), head = in.h << p.page_shift;
+      const int key = in.key(p, in_unit), head = in.h << p.page_shift;
       if (in_page >= S::kUnit - 1) {   // one page holds the unit: its keys are one run
         if (pages) {
           const int page = __shfl_sync(0xffffffffu, pid, __ffs(pages) - 1);
@@ -381,8 +399,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
                        16 * ((lane >> 4) ^ (kChunks == 2 ? (lane >> 2) & 1 : (lane >> 1) & 3));
   float* const factors = reinterpret_cast<float*>(ring + S::kStages * S::kStageBytes);   // [key][keys' blocks, values']
 
-  int stage = 0;
-  for (int at = 0; at < count;) {
+  int stage = 0, at = 0;
+  do {
     // ---- one item: rows, queries ----
     const int end = min(count, cur.end), from = at;
     const int len = cur.len, h = cur.h, row0 = cur.rt * S::kRows;
@@ -456,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
       }
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
       const unsigned pages = lds32(sk + kPages);
-      const int key0 = cur.key(at);
+      const int key0 = cur.key(p, at);
 
       // The unit's scales as fp32: the keys' own, the values' as weight factors 2^(15 + e - E). A
       // lane takes keys lane (and lane + 32). A key that no row sees counts as scale 0: what
@@ -655,6 +673,58 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
       __syncwarp();
     }
 
+    // ---- an item that several warps of the CTA shared ----
+    if (p.whole > 1) {
+      const int ways = p.whole, way = warp % ways;
+      cp_async_wait<0>();
+      __syncwarp();
+      constexpr int kWarpBytes = S::kStages * S::kStageBytes + S::kFactors;
+      float* const mine = reinterpret_cast<float*>(ring);   // the ring is done with: sums [row][D]
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float sum = l[i][x];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          const int r = 8 * i + 2 * t + x;
+          if (g == 0) reinterpret_cast<float2*>(factors)[r] = make_float2(m[i][x] * qs[i][x], sum);
+#pragma unroll
+          for (int k = 0; k < S::kBlocks; ++k) {
+            const float f = ex2(static_cast<float>((E[k] >> 23) - 142));
+            *reinterpret_cast<float4*>(mine + r * D + 32 * k + 4 * g) =
+                make_float4(o[i][k][0][x] * f, o[i][k][0][x + 2] * f, o[i][k][1][x] * f, o[i][k][1][x + 2] * f);
+          }
+        }
+      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + warp / ways), "r"(32 * ways) : "memory");
+      const uint8_t* const all = smem + (warp - way) * kWarpBytes;
+      constexpr int kCols = D / 32;   // columns of a lane
+      for (int r = way; r < S::kRows && row0 + r < p.R; r += ways) {
+        const int row = row0 + r, hd = h * p.G + row % p.G;
+        float top = -INFINITY;
+        for (int w = 0; w < ways; ++w)
+          top = fmaxf(top, reinterpret_cast<const float2*>(all + w * kWarpBytes + S::kStages * S::kStageBytes)[r].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = p.sinks ? ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base) : 0.f, v[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) v[c] = 0.f;
+        for (int w = 0; w < ways; ++w) {
+          const float2 ml = reinterpret_cast<const float2*>(all + w * kWarpBytes + S::kStages * S::kStageBytes)[r];
+          const float f = ex2(ml.x - base);
+          sum = fmaf(f, ml.y, sum);
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            v[c] = fmaf(f, reinterpret_cast<const float*>(all + w * kWarpBytes)[r * D + kCols * lane + c], v[c]);
+        }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        uint16_t* dst = p.out + ((static_cast<int64_t>(cur.b) * p.Lq + row / p.G) * p.Hkv * p.G + hd) * D + kCols * lane;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 2) *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16(v[c] * inv, v[c + 1] * inv);
+      }
+      return;
+    }
+
     // ---- the item's end in this run ----
     const bool opened = from > 0 || start == 0;   // the item's first unit is in this run
     const bool whole = opened && cur.end <= count;
@@ -701,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) kv_attention_ke
                            : make_int4(static_cast<int>(slot), run, run + (cur.end - 1) / s_per, 0);
     }
     if (at == cur.end && at < count) cur.next(p);
-  }
+  } while (at < count);
   cp_async_wait<0>();
 }
 
@@ -779,7 +849,6 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
 namespace {
 
 int tiles_n(int R) { return R > 8 ? 2 : 1; }   // 8-row tiles of an item
-int ctas_per_sm(int D, int nt) { return D == 64 || nt == 1 ? 2 : 1; }
 
 struct Layout {
   size_t desc, ml, part, bytes;
@@ -787,7 +856,7 @@ struct Layout {
 
 Layout layout(int64_t items, int R, int D, int sms) {
   const int nt = tiles_n(R);
-  const size_t rows = static_cast<size_t>(2) * sms * ctas_per_sm(D, nt) * kva::kWarps * 8 * nt;   // two slots a run
+  const size_t rows = static_cast<size_t>(2) * sms * kva::warps(D, nt) * 8 * nt;   // two slots a run
   Layout l;
   l.desc = 0;
   l.ml = (items * sizeof(int4) + 255) & ~static_cast<size_t>(255);
@@ -803,14 +872,23 @@ cudaError_t launch(KvAttentionArgs p, int sms, cudaStream_t st, int* launches) {
   static SmemLimit limit;
   cudaError_t e = limit.raise(kv_attention_kernel<D, NT>, S::kSmem);
   if (e != cudaSuccess) return e;
-  const int grid = sms * S::kCtas;
-  // Items of at most four units (a short window or a short table) are not cut: a warp takes
-  // them whole, nothing is left to join, and no run has to be found.
+  const int grid = sms;
+  // Items of at most four units (a short window or a short table) stay in one CTA: nothing is left
+  // for a second kernel, and no run has to be found. Where that still leaves half of the warps
+  // without work, two or four share an item and join through shared memory (a window of 128
+  // keys, 8 heads of 64: one sequence 9.0 -> 6.2 us with four; 96 sequences 11.0 us with one, 11.8
+  // with two).
   const int64_t keys = static_cast<int64_t>(p.max_pages) << p.page_shift;
   const int64_t reach = p.window > 0 ? std::min<int64_t>(keys, static_cast<int64_t>(p.window) + p.Lq - 1) : keys;
-  p.whole = cdiv(reach, S::kUnit) + (reach < keys ? 1 : 0) <= 4;
+  const int64_t most = cdiv(reach, S::kUnit) + (reach < keys ? 1 : 0);   // units of an item
+  p.whole = 0;
+  if (most <= 4) {
+    const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * p.RT, warps = static_cast<int64_t>(grid) * S::kWarps;
+    p.whole = most > 2 && 8 * items <= warps ? 4 : most > 1 && 4 * items <= warps ? 2 : 1;
+  }
+  p.unit_step = S::kUnit * std::max(p.whole, 1);
   *launches = p.whole ? 1 : 2;
-  kv_attention_kernel<D, NT><<<grid, kThreads, S::kSmem, st>>>(p);
+  kv_attention_kernel<D, NT><<<grid, S::kThreads, S::kSmem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess || p.whole) return e;
   // Few items are cut into many parts each: a CTA per row, its warps over the parts.
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * p.RT;

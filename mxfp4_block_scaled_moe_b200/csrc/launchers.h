@@ -249,8 +249,8 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t st);
 
-// attention over that cache (csrc/kv_attention.cu): D 64 or 128. launch_kv_attention sets RT,
-// whole and the workspace pointers.
+// attention over that cache (csrc/kv_attention.cu): D 64 or 128. launch_kv_attention sets the
+// fields from RT on.
 struct KvAttentionArgs {
   const uint16_t* q;
   int64_t q_stride;             // elements between tokens
@@ -270,7 +270,8 @@ struct KvAttentionArgs {
   uint16_t* out;                // (B, Lq, Hkv * G, D)
   int* err;
   int RT;                       // row tiles of an item
-  int whole;                    // items are not cut over warps
+  int whole;                    // 0: items are cut over runs; else warps of one CTA that share an item
+  int unit_step;                // keys from a warp's unit of an item to its next
   int4* desc;
   float2* part_ml;
   float* part;

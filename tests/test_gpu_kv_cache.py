@@ -188,6 +188,10 @@ CASES = [
     dict(lens=[1000, 128, 129, 127, 1], Lq=1, Hq=64, Hkv=8, D=64, page=16, window=128, sinks=True),
     dict(lens=[1000, 40, 3], Lq=3, Hq=8, Hkv=2, D=128, page=32, window=37),
     dict(lens=[500, 33], Lq=2, Hq=8, Hkv=1, D=64, page=16, window=1),
+    dict(lens=[150 + i % 90 for i in range(120)], Lq=1, Hq=16, Hkv=8, D=64, page=16, window=128, sinks=True),
+    dict(lens=[150 + i % 90 for i in range(400)], Lq=1, Hq=16, Hkv=8, D=64, page=16, window=128),
+    dict(lens=[90, 0, 64, 5], Lq=1, Hq=8, Hkv=1, D=128, page=32, sinks=True),             # a short table
+    dict(lens=[90, 0, 64, 5] * 90, Lq=1, Hq=16, Hkv=8, D=128, page=32),
     dict(lens=[20000], Lq=1, Hq=8, Hkv=1, D=64, page=256),
     dict(lens=[9] * 700, Lq=1, Hq=2, Hkv=2, D=64, page=16),
     dict(lens=[40000, 11], Lq=2, Hq=8, Hkv=2, D=128, page=64),
