@@ -236,6 +236,54 @@ def test_attention_query_magnitudes(B):
     c.check(out)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30])
+def test_attention_unusual_scales(B, scale):
+    c = Case(B, [70, 33, 500], 1, 8, 2, 64, 16, window=40, sinks=True)
+    c.check(c.run(B, scale=scale), scale=scale)
+
+
+def test_attention_sinks_alone_and_extreme_sinks(B):
+    c = Case(B, [0, 40], 1, 8, 1, 64, 16, sinks=True)
+    c.sinks = torch.tensor([-math.inf, -1e30, -200.0, 0.0, 200.0, 1e30, 3.0, -3.0], device="cuda")
+    out = c.run(B)
+    assert not bool(out[0].any())
+    c.check(out)
+
+
+def test_nan_stays_in_its_row(B):
+    c = Case(B, [100], 1, 8, 1, 64, 16)
+    want = c.run(B)
+    c.q[0, 0, 3, 5] = float("nan")
+    out = c.run(B)
+    assert bool(out[0, 0, 3].isnan().all())
+    keep = [i for i in range(8) if i != 3]
+    assert torch.equal(out[0, 0, keep], want[0, 0, keep])
+
+
+def test_offsets_past_32_bits(B):
+    """Codes of more than 4 GiB each for keys and values: the last pages are reached."""
+    page, Hkv, D, n = 256, 8, 64, 700
+    pages = (1 << 32) // (Hkv * page * D // 2) + 5
+    cache = [torch.empty(pages, Hkv, page, d, dtype=torch.uint8, device="cuda") for d in (D // 2, D // 32) * 2]
+    assert cache[0].numel() > 1 << 32
+    c = Case(B, [n], 1, 64, Hkv, D, page)
+    table = torch.tensor([[pages - 1, 2, pages - 2]], dtype=torch.int32, device="cuda")
+    pos = torch.arange(n, device="cuda")
+    slots = table[0].long()[pos // page] * page + pos % page
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn(n, Hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    B.mxfp4_kv_append(k, v, slots, *cache)
+    small = [torch.empty(3, Hkv, page, d, dtype=torch.uint8, device="cuda") for d in (D // 2, D // 32) * 2]
+    B.mxfp4_kv_append(k, v, pos, *small)
+    for big, s in zip(cache, small):
+        for i, p in enumerate(table[0].tolist()):
+            m = min(page, n - i * page)
+            assert torch.equal(big[p, :, :m], s[i, :, :m])
+    want = B.mxfp4_kv_attention(c.q, *small, torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda"), c.lens)
+    assert torch.equal(B.mxfp4_kv_attention(c.q, *cache, table, c.lens), want)
+    B.mxmoe_check()
+
+
 def test_attention_pages_that_are_gone(B):
     c = Case(B, [900, 64], 2, 16, 2, 64, 16, window=100)
     keep = c.table.clone()

@@ -142,6 +142,10 @@ def test_streams_graph_and_empty(B):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, -want)
+    one = x[0].clone()                                    # a single row without a token axis
+    q, sc, _ = B.rmsnorm_residual_fp8(one, w)
+    assert q.shape == one.shape and sc.shape == ()
+    _check_q(q, _norm64(one, w) / sc.double())
     e = torch.empty(0, 2880, device="cuda", dtype=torch.bfloat16)
     assert B.rmsnorm_residual(e, w, e)[0].shape == (0, 2880)
     assert B.rmsnorm_residual_fp8(e, w)[1].shape == (0,)
