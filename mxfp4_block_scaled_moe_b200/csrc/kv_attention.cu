@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
   constexpr int kCols = D / 32;   // columns of a lane
   extern __shared__ __align__(16) uint8_t smem[];   // one-row sets only: a CTA without any fits beside the kernel before
   float(*const s_o)[D] = reinterpret_cast<float(*)[D]>(smem);
-  float* const s_l = reinterpret_cast<float*>(smem) + kJoinThreads / 32 * D;
+  float2* const s_ml = reinterpret_cast<float2*>(smem + kJoinThreads / 32 * D * sizeof(float));
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sets = S::kRows / rows;   // CTAs of an item
@@ -799,40 +799,64 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
   for (int r = shared ? first_row : first_row + warp; r < first_row + rows; r += kJoinThreads / 32) {
     const int row = row0 + r;
     if (row >= p.R) break;
-    const int lo = d.y + (shared ? warp : 0), step = shared ? kJoinThreads / 32 : 1;
+    // the parts of this warp, eight at a time: maxima, sums and columns on their way at once
+    const int step = shared ? kJoinThreads / 32 : 1;
     float top = -INFINITY, sum = 0.f, v[kCols];
-    for (int run = d.y + lane; run <= d.z; run += 32) {
-      const int64_t slot = run == d.y ? d.x : 2 * static_cast<int64_t>(run);
-      top = fmaxf(top, p.part_ml[slot * S::kRows + r].x);
-    }
-    top = warp_max(top);
-    const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int c = 0; c < kCols; ++c) v[c] = 0.f;
-#pragma unroll 4
-    for (int run = lo; run <= d.z; run += step) {
-      const int64_t slot = run == d.y ? d.x : 2 * static_cast<int64_t>(run);
-      const float2 ml = p.part_ml[slot * S::kRows + r];
-      const float* src = p.part + (slot * S::kRows + r) * D + kCols * lane;
-      const float f = ex2(ml.x - base);
-      sum = fmaf(f, ml.y, sum);
+    for (int first = d.y + (shared ? warp : 0); first <= d.z; first += 8 * step) {
+      float2 ml[8];
+      float x[8][kCols];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) v[c] = fmaf(f, src[c], v[c]);
+      for (int i = 0; i < 8; ++i) {
+        const int run = first + i * step;
+        ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
+        if (run <= d.z) {
+          const int64_t at = (run == d.y ? d.x : 2 * static_cast<int64_t>(run)) * S::kRows + r;
+          ml[i] = p.part_ml[at];
+#pragma unroll
+          for (int c = 0; c < kCols; c += 2)
+            *reinterpret_cast<float2*>(&x[i][c]) = *reinterpret_cast<const float2*>(p.part + at * D + kCols * lane + c);
+        }
+      }
+      float next = top;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) next = fmaxf(next, ml[i].x);
+      const float base = next == -INFINITY ? 0.f : next, old = ex2(top - base);
+      top = next;
+      sum *= old;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) v[c] *= old;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = ex2(ml[i].x - base);
+        sum = fmaf(f, ml[i].y, sum);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) v[c] = fmaf(f, x[i][c], v[c]);
+      }
     }
+    float base = top == -INFINITY ? 0.f : top;
     if (shared) {
 #pragma unroll
       for (int c = 0; c < kCols; ++c) s_o[warp][kCols * lane + c] = v[c];
-      if (lane == 0) s_l[warp] = sum;
+      if (lane == 0) s_ml[warp] = make_float2(top, sum);
       __syncthreads();
       if (warp > 0) return;
+      top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_ml[w].x);
+      base = top == -INFINITY ? 0.f : top;
       sum = 0.f;
 #pragma unroll
       for (int c = 0; c < kCols; ++c) v[c] = 0.f;
 #pragma unroll
       for (int w = 0; w < kJoinThreads / 32; ++w) {
-        sum += s_l[w];
+        const float f = ex2(s_ml[w].x - base);
+        sum = fmaf(f, s_ml[w].y, sum);
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) v[c] += s_o[w][kCols * lane + c];
+        for (int c = 0; c < kCols; ++c) v[c] = fmaf(f, s_o[w][kCols * lane + c], v[c]);
       }
     }
     const int hd = h * p.G + row % p.G;
@@ -896,7 +920,7 @@ cudaError_t launch(KvAttentionArgs p, int sms, cudaStream_t st, int* launches) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * (S::kRows / rows)));
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = rows == 1 ? kJoinThreads / 32 * (D + 1) * sizeof(float) : 0;
+  cfg.dynamicSmemBytes = rows == 1 ? kJoinThreads / 32 * (D + 2) * sizeof(float) : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

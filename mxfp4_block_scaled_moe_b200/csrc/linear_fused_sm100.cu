@@ -507,12 +507,21 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
     __syncwarp();
     tc_fence_after();
     const int q = warp & 3;
-    for (int c0 = 0; c0 < BN && t0 + c0 < p.T; c0 += 8) {
-      uint32_t v[8];
-      tc_ld_32x32b_x8(tmem + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
-      tc_wait_ld(v);
+    if constexpr (BN >= 32) {
+      for (int c0 = 0; c0 < BN && t0 + c0 < p.T; c0 += 32) {
+        uint32_t v[32];
+        tc_ld_32x32b_x32(tmem + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sums[(c0 + i) * BM + 32 * q + lane] = __uint_as_float(v[i]);
+        for (int i = 0; i < 32; ++i) sums[(c0 + i) * BM + 32 * q + lane] = __uint_as_float(v[i]);
+      }
+    } else {
+      for (int c0 = 0; c0 < BN && t0 + c0 < p.T; c0 += 8) {
+        uint32_t v[8];
+        tc_ld_32x32b_x8(tmem + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
+        tc_wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[(c0 + i) * BM + 32 * q + lane] = __uint_as_float(v[i]);
+      }
     }
     tc_fence_before();
   }
@@ -529,13 +538,21 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
     const int tok = gi / (BM / 8), n = m0 + 8 * (gi % (BM / 8));
     if (gi != g0) fetch(gi);
     if (n >= p.N) continue;
+    float4 x[kMaxK], y[kMaxK];   // all ranks' sums on their way at once
+#pragma unroll
+    for (int r = 0; r < kMaxK; ++r)
+      if (r < ks) {
+        const uint32_t at = peer_addr(base + 4 * (tok * BM + 8 * (gi % (BM / 8))), r);
+        x[r] = ld_peer(at);
+        y[r] = ld_peer(at + 16);
+      }
     float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int r = 0; r < ks; ++r) {   // in rank order
-      const uint32_t at = peer_addr(base + 4 * (tok * BM + 8 * (gi % (BM / 8))), r);
-      const float4 x = ld_peer(at), y = ld_peer(at + 16);
-      a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
-      a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
-    }
+#pragma unroll
+    for (int r = 0; r < kMaxK; ++r)
+      if (r < ks) {              // added in rank order
+        a[0] += x[r].x; a[1] += x[r].y; a[2] += x[r].z; a[3] += x[r].w;
+        a[4] += y[r].x; a[5] += y[r].y; a[6] += y[r].z; a[7] += y[r].w;
+      }
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] *= sx;
     finish8<kAct>(p, t0 + tok, n, a, cols, res);
