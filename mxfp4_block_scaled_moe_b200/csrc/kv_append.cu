@@ -50,6 +50,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(KvAppendArgs p, int
   const int units = (p.Hkv * row_vecs) << shift;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) << shift;
   constexpr int kAtOnce = 2;
+  griddep_launch_dependents();
+  griddep_wait();
   for (int first = threadIdx.x; first - static_cast<int>(threadIdx.x) < units; first += kAtOnce * kThreads) {
     int64_t slot[kAtOnce];
     uint4 k[kAtOnce], v[kAtOnce];
@@ -103,13 +105,8 @@ cudaError_t launch_kv_append(const KvAppendArgs& p, int sms, cudaStream_t st) {
   int shift = 0;
   while ((vecs << shift) < 2 * kThreads && (static_cast<int64_t>(p.T) >> (shift + 1)) >= 2 * sms) ++shift;
   const unsigned grid = static_cast<unsigned>(cdiv(p.T, static_cast<int64_t>(1) << shift));
-  if (p.D == 64)
-    kv_append_kernel<8><<<grid, kThreads, 0, st>>>(p, shift);
-  else if (p.D == 128)
-    kv_append_kernel<16><<<grid, kThreads, 0, st>>>(p, shift);
-  else
-    kv_append_kernel<0><<<grid, kThreads, 0, st>>>(p, shift);
-  return cudaGetLastError();
+  const auto kernel = p.D == 64 ? kv_append_kernel<8> : p.D == 128 ? kv_append_kernel<16> : kv_append_kernel<0>;
+  return launch_early(kernel, dim3(grid), kThreads, 0, 0, st, p, shift);
 }
 
 }  // namespace mxmoe

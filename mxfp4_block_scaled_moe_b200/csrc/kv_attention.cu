@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int per_seq = p.Hkv * p.RT;
   griddep_launch_dependents();   // the joining kernel may take its places; it waits for this one's end
+  griddep_wait();
 
   // ---- this warp's run: `count` units from `cur` on, whose item may have begun before it ----
   // neighbouring runs go to different SMs, so that a short line still uses all of them
@@ -785,6 +786,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
   extern __shared__ __align__(16) uint8_t smem[];   // one-row sets only: a CTA without any fits beside the kernel before
   float(*const s_o)[D] = reinterpret_cast<float(*)[D]>(smem);
   float2* const s_ml = reinterpret_cast<float2*>(smem + kJoinThreads / 32 * D * sizeof(float));
+  griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sets = S::kRows / rows;   // CTAs of an item
@@ -912,22 +914,13 @@ cudaError_t launch(KvAttentionArgs p, int sms, cudaStream_t st, int* launches) {
   }
   p.unit_step = S::kUnit * std::max(p.whole, 1);
   *launches = p.whole ? 1 : 2;
-  kv_attention_kernel<D, NT><<<grid, S::kThreads, S::kSmem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.whole) return e;
+  e = launch_early(kv_attention_kernel<D, NT>, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, 0, st, p);
+  if (e != cudaSuccess || p.whole) return e;
   // Few items are cut into many parts each: a CTA per row, its warps over the parts.
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * p.RT;
   const int rows = items < 2 * sms ? 1 : S::kRows;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items * (S::kRows / rows)));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = rows == 1 ? kJoinThreads / 32 * (D + 2) * sizeof(float) : 0;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, NT>, p, rows);
+  return launch_early(kv_attention_join_kernel<D, NT>, dim3(static_cast<unsigned>(items * (S::kRows / rows))), kJoinThreads,
+                      rows == 1 ? kJoinThreads / 32 * (D + 2) * sizeof(float) : 0, 0, st, p, rows);
 }
 
 }  // namespace

@@ -8,6 +8,30 @@
 
 namespace mxmoe {
 
+// Launches a kernel that may start before the one before it in the stream has ended (programmatic
+// stream serialization), in clusters of `cluster` CTAs along x if that is not 0. The kernel
+// calls griddep_wait() in every thread before its first access to memory that another kernel
+// may write or read. The operators that a decode step chains also let their successor start
+// early (griddep_launch_dependents()), so that a chain of them pays one launch latency.
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
+                         Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // Raises a kernel's dynamic shared-memory limit, once per device (one static object a kernel).
 class SmemLimit {
  public:

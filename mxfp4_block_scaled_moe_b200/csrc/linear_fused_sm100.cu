@@ -219,7 +219,7 @@ constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiWarps * kTurn + 256;
 }  // namespace pair
 
 template <int kAct>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+__global__ void __launch_bounds__(pair::kThreads, 1)
 fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                        const LinearFusedArgs p) {
   using namespace pair;
@@ -259,6 +259,8 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  griddep_launch_dependents();   // only now: a successor's CTA beside this one must not get the tensor memory first
+  griddep_wait();
 
   const int n_tiles = (p.N + BN - 1) / BN, units = ((p.T + BM - 1) / BM) * n_tiles, nk = (p.K + BK - 1) / BK;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -456,6 +458,8 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  griddep_launch_dependents();   // only now: a successor's CTA beside this one must not get the tensor memory first
+  griddep_wait();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -587,8 +591,8 @@ cudaError_t launch_pair(const LinearFusedArgs& p, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t units = cdiv(p.T, pair::BM) * cdiv(p.N, pair::BN);
   const int grid = 2 * static_cast<int>(std::min<int64_t>(units, sms / 2));
-  fp8_linear_pair_kernel<kAct><<<grid, pair::kThreads, pair::kSmemBytes, st>>>(mx, mw, p);
-  return cudaGetLastError();
+  return launch_early(fp8_linear_pair_kernel<kAct>, dim3(static_cast<unsigned>(grid)), pair::kThreads, pair::kSmemBytes, 2,
+                      st, mx, mw, p);
 }
 
 // Clusters of ks CTAs of the split kernel that the device holds at once: a cluster lies in one
@@ -643,19 +647,8 @@ cudaError_t launch_split(const LinearFusedArgs& p, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int m_tiles = static_cast<int>(cdiv(p.N, split::BM)), t_tiles = static_cast<int>(cdiv(p.T, BN));
   const int ks = split_ranges<BN>(static_cast<int64_t>(m_tiles) * t_tiles, p.K, sms);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(m_tiles * ks), static_cast<unsigned>(t_tiles));
-  cfg.blockDim = dim3(split::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_linear_split_kernel<BN, kAct>, mw, mx, p, ks);
+  return launch_early(fp8_linear_split_kernel<BN, kAct>, dim3(static_cast<unsigned>(m_tiles * ks), static_cast<unsigned>(t_tiles)),
+                      split::kThreads, smem, ks, st, mw, mx, p, ks);
 }
 
 // Which kernel for more than 128 tokens: the shorter by what each measured on a B200 over 22 sizes,

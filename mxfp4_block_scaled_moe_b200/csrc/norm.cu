@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(kWarp ? 128 : 512) rmsnorm_kernel(NormArgs p) 
   const int lanes = kWarp ? 32 : blockDim.x;
   const int tid = kWarp ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t t = kWarp ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  griddep_launch_dependents();
+  griddep_wait();
   if (kWarp && t >= p.T) return;
   const int nv = p.H >> 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -166,11 +168,8 @@ __global__ void __launch_bounds__(kWarp ? 128 : 512) rmsnorm_kernel(NormArgs p) 
 
 template <int kVec, bool kWarp>
 cudaError_t launch_variant(const NormArgs& p, unsigned grid, int threads, cudaStream_t st) {
-  if (p.q_scale)
-    rmsnorm_kernel<kVec, kWarp, true><<<grid, threads, 0, st>>>(p);
-  else
-    rmsnorm_kernel<kVec, kWarp, false><<<grid, threads, 0, st>>>(p);
-  return cudaGetLastError();
+  return p.q_scale ? launch_early(rmsnorm_kernel<kVec, kWarp, true>, dim3(grid), threads, 0, 0, st, p)
+                   : launch_early(rmsnorm_kernel<kVec, kWarp, false>, dim3(grid), threads, 0, 0, st, p);
 }
 
 }  // namespace
