@@ -37,6 +37,10 @@
  *    it allocates, so the first call at a new maximum size must not be inside a CUDA
  *    graph capture. Calls that share a device must not overlap on the GPU (the
  *    workspace is shared): issue them on one stream, or order the streams.
+ *    rmsnorm_residual, fp8_linear_fused, mxfp4_kv_append and mxfp4_kv_attention do not use it:
+ *    such calls may overlap each other and any other call. Like every entry point they
+ *    allocate the device's error word if theirs is the first call on it, so that one call
+ *    has to come before any capture.
  */
 #ifndef MXFP4_MOE_H
 #define MXFP4_MOE_H

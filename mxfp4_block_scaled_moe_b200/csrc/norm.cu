@@ -14,7 +14,8 @@
 //
 // One CTA per row, or one warp per row for many short rows; the rule and what it measured
 // stand at launch_rmsnorm. 4096 x 2880 with a residual and a static scale (82.6 MB): 17.2 us,
-// 4.8 TB/s; 16384 x 2880 to bf16 (377 MB): 60 us, 6.3 TB/s.
+// 4.8 TB/s; 16384 x 2880 to bf16 (377 MB): 60 us, 6.3 TB/s. CTAs that walk the rows with the next
+// one's loads in flight were no faster (17.5 and 69 us).
 #include <algorithm>
 #include <cfloat>
 
