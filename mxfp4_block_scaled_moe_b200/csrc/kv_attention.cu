@@ -179,6 +179,11 @@ __device__ __forceinline__ uint32_t exponent_of(uint32_t word, int k) {
   return (k < 3 ? word << (23 - 8 * k) : word >> 1) & 0x7F800000u;
 }
 
+// r / G for the rows of an item: r G < 2^32, so the rounded-up reciprocal is exact
+__device__ __forceinline__ int query_of(const KvAttentionArgs& p, int r) {
+  return p.G == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.g_reciprocal));
+}
+
 // ------------------------------------------------------------------- work line -----
 __device__ __forceinline__ int seq_len(const KvAttentionArgs& p, int b) {
   const int n = __ldg(p.seq_lens + b);
@@ -231,6 +236,32 @@ struct Cursor {
   }
 };
 
+// Run number `run` of `runs` equal ones of a line of n units: its units [t0, t0 + count).
+struct Run {
+  int per, t0, count;
+};
+template <int kUnit>
+__device__ __forceinline__ Run run_of(int n, int runs, int run) {
+  Run r;
+  r.per = max(64 / kUnit, n / runs + (n % runs ? 1 : 0));   // 64 keys at least
+  r.t0 = static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(r.per) * run));
+  r.count = min(r.per, n - r.t0);
+  return r;
+}
+
+// Opens the item of sequence b that holds its unit `into`; returns where the item starts, counted
+// from that unit (0 or before it).
+template <int kUnit>
+__device__ __forceinline__ int open_at(const KvAttentionArgs& p, Cursor<kUnit>& c, int b, int into) {
+  c.b = b;
+  const int units = units_of<kUnit>(p, seq_len(p, b)), j = into / units;
+  c.h = p.RT == 1 ? j : j / p.RT;
+  c.rt = p.RT == 1 ? 0 : j % p.RT;
+  const int start = j * units - into;
+  c.open(p, start);
+  return start;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel(const KvAttentionArgs p) {
   using S = Shape<D, NT>;
@@ -238,7 +269,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_sum[kWarps];
   __shared__ int s_pre[kThreads];
-  __shared__ int s_per;
+  __shared__ int s_per[kWarps];   // a run's units; each warp's own word
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int per_seq = p.Hkv * p.RT;
   griddep_launch_dependents();   // the joining kernel may take its places; it waits for this one's end
@@ -269,10 +300,45 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
     cur.h = i0 % per_seq / p.RT;
     cur.rt = i0 % p.RT;
     cur.open(p, 0);
+  } else if (p.B <= 128) {   // each warp by itself, four sequences a lane
+    int pre[4], n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = 32 * i + lane;
+      pre[i] = b < p.B ? units_of<S::kUnit>(p, seq_len(p, b)) * per_seq : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (32 * i >= p.B) break;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, pre[i], o);
+        if (lane >= o) pre[i] += x;
+      }
+      pre[i] += n;
+      n = __shfl_sync(0xffffffffu, pre[i], 31);
+    }
+    const Run r = run_of<S::kUnit>(n, runs, run);
+    count = r.count;
+    if (count == 0) return;
+    int before = 0;   // units before the chunk of 32 sequences
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (cur.b >= 0 || 32 * i >= p.B) break;
+      const unsigned past = __ballot_sync(0xffffffffu, pre[i] > r.t0);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        const int from = at ? __shfl_sync(0xffffffffu, pre[i], at - 1) : before;
+        start = open_at<S::kUnit>(p, cur, 32 * i + at, r.t0 - from);
+      }
+      before = __shfl_sync(0xffffffffu, pre[i], 31);
+    }
+    if (lane == 0) s_per[warp] = r.per;
+    __syncwarp();
   } else {
     // pass 0 counts the line's units, pass 1 finds the run's first; a batch of one chunk of
     // kThreads sequences needs its prefix sums once
-    int per = 0, t0 = 0;
+    Run r{};
     for (int pass = p.B > kThreads ? 0 : 1; pass < 2; ++pass) {
       int base = 0;   // units before this chunk of sequences
       for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -295,34 +361,26 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
         s_pre[threadIdx.x] = base + pre;
         __syncthreads();
         if (pass == 0 || p.B <= kThreads) {
-          const int n = base + all;
-          per = max(64 / S::kUnit, n / runs + (n % runs ? 1 : 0));   // 64 keys at least
-          t0 = static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(per) * run));
-          count = min(per, n - t0);
+          r = run_of<S::kUnit>(base + all, runs, run);
+          count = r.count;
         }
-        if (pass == 1 && count > 0 && base <= t0 && t0 < base + all) {
+        if (pass == 1 && count > 0 && base <= r.t0 && r.t0 < base + all) {
           // the first sequence of the chunk whose units end after t0
 #pragma unroll
           for (int i = 0; i < kThreads / 32; ++i) {
-            const unsigned past = __ballot_sync(0xffffffffu, s_pre[32 * i + lane] > t0);
+            const unsigned past = __ballot_sync(0xffffffffu, s_pre[32 * i + lane] > r.t0);
             if (past && cur.b < 0) {
               const int at = 32 * i + __ffs(past) - 1;
-              cur.b = b0 + at;
-              const int units = units_of<S::kUnit>(p, seq_len(p, cur.b));
-              const int into = t0 - (s_pre[at] - units * per_seq), j = into / units;
-              cur.h = j / p.RT;
-              cur.rt = j % p.RT;
-              start = j * units - into;
-              cur.open(p, start);
+              start = open_at<S::kUnit>(p, cur, b0 + at, r.t0 - (at ? s_pre[at - 1] : base));
             }
           }
         }
         base += all;
       }
     }
-    if (threadIdx.x == 0) s_per = per;
-    __syncthreads();
     if (count == 0) return;
+    if (lane == 0) s_per[warp] = r.per;
+    __syncwarp();
   }
 
   // ---- this warp's ring of units ----
@@ -399,7 +457,23 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
     cp_async_commit();
     look();
   };
+  // an item's queries, 16 bytes of a row and block a lane; fetched ahead of their use: the first
+  // item's beside its first pages, another's while the one before it is written
+  uint4 raw[NT][S::kBlocks];
+  auto load_q = [&](const Cursor<S::kUnit>& c) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int r = c.rt * S::kRows + 8 * i + g;
+      const bool real = r < p.R;
+      const int qi = real ? query_of(p, r) : 0, hd = c.h * p.G + (real ? r - qi * p.G : 0);
+      const uint16_t* src = p.q + (static_cast<int64_t>(c.b) * p.Lq + qi) * p.q_stride + static_cast<int64_t>(hd) * D;
+#pragma unroll
+      for (int k = 0; k < S::kBlocks; ++k)
+        raw[i][k] = real ? __ldg(reinterpret_cast<const uint4*>(src + 32 * k + 8 * t)) : make_uint4(0, 0, 0, 0);
+    }
+  };
   look();
+  load_q(cur);
 #pragma unroll
   for (int s = 0; s < S::kStages - 1; ++s) issue(s);
 
@@ -418,18 +492,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
     float qs[NT][2];                      // of rows 2t, 2t + 1: score scale in base 2, undoing the f16 shift
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int r = row0 + 8 * i + g;
-      const bool real = r < p.R;
-      const int qi = real ? r / p.G : 0, hd = h * p.G + (real ? r % p.G : 0);
-      const uint16_t* src = p.q + (static_cast<int64_t>(cur.b) * p.Lq + qi) * p.q_stride + static_cast<int64_t>(hd) * D;
-      uint4 u[S::kBlocks];
       uint32_t top = 0;
 #pragma unroll
-      for (int k = 0; k < S::kBlocks; ++k)
-        u[k] = real ? __ldg(reinterpret_cast<const uint4*>(src + 32 * k + 8 * t)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
       for (int k = 0; k < S::kBlocks; ++k) {
-        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+        const uint32_t w[4] = {raw[i][k].x, raw[i][k].y, raw[i][k].z, raw[i][k].w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) top = max(top, max((w[x] << 16) & 0x7FFF0000u, w[x] & 0x7FFF0000u));
       }
@@ -441,7 +507,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
       const float down = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
 #pragma unroll
       for (int k = 0; k < S::kBlocks; ++k) {
-        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+        const uint32_t w[4] = {raw[i][k].x, raw[i][k].y, raw[i][k].z, raw[i][k].w};
 #pragma unroll
         for (int x = 0; x < 4; ++x)
           qf[i][k][x] = pack_f16(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xFFFF0000u) * up);
@@ -451,8 +517,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
       qs[i][1] = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2, 0x1p-126f);
     }
     // keys that some row (seen) and that every row (full) of the tile sees
-    const int hi_first = len - p.Lq + row0 / p.G + 1;
-    const int hi_last = len - p.Lq + (min(row0 + S::kRows, p.R) - 1) / p.G + 1;
+    const int hi_first = len - p.Lq + query_of(p, row0) + 1;
+    const int hi_last = len - p.Lq + query_of(p, min(row0 + S::kRows, p.R) - 1) + 1;
     const int seen_lo = p.window > 0 ? max(0, hi_first - p.window) : 0, seen_hi = max(hi_last, 0);
     const int full_lo = p.window > 0 ? max(0, hi_last - p.window) : 0, full_hi = hi_first;
 
@@ -579,7 +645,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int row = row0 + 8 * i + 2 * t + x;
-            hi[x] = row < p.R ? len - p.Lq + row / p.G + 1 : 0;
+            hi[x] = row < p.R ? len - p.Lq + query_of(p, row) + 1 : 0;
             lo[x] = p.window > 0 ? hi[x] - p.window : 0;
           }
 #pragma unroll
@@ -711,7 +777,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
       const uint8_t* const all = smem + (warp - way) * kWarpBytes;
       constexpr int kCols = D / 32;   // columns of a lane
       for (int r = way; r < S::kRows && row0 + r < p.R; r += ways) {
-        const int row = row0 + r, hd = h * p.G + row % p.G;
+        const int row = row0 + r, qi = query_of(p, row), hd = h * p.G + row - qi * p.G;
         float top = -INFINITY;
         for (int w = 0; w < ways; ++w)
           top = fmaxf(top, reinterpret_cast<const float2*>(all + w * kWarpBytes + S::kStages * S::kStageBytes)[r].x);
@@ -728,7 +794,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
             v[c] = fmaf(f, reinterpret_cast<const float*>(all + w * kWarpBytes)[r * D + kCols * lane + c], v[c]);
         }
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        uint16_t* dst = p.out + ((static_cast<int64_t>(cur.b) * p.Lq + row / p.G) * p.Hkv * p.G + hd) * D + kCols * lane;
+        uint16_t* dst = p.out + ((static_cast<int64_t>(cur.b) * p.Lq + qi) * p.Hkv * p.G + hd) * D + kCols * lane;
 #pragma unroll
         for (int c = 0; c < kCols; c += 2) *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16(v[c] * inv, v[c + 1] * inv);
       }
@@ -736,6 +802,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
     }
 
     // ---- the item's end in this run ----
+    Cursor<S::kUnit> following = cur;
+    if (at == cur.end && at < count) {
+      following.next(p);
+      load_q(following);
+    }
     const bool opened = from > 0 || start == 0;   // the item's first unit is in this run
     const bool whole = opened && cur.end <= count;
     const int64_t slot = 2 * static_cast<int64_t>(run) + (from > 0 ? 1 : 0);
@@ -750,11 +821,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
         const int r = 8 * i + 2 * t + x, row = row0 + r;
         const int c0 = 4 * g;   // the lane's four columns of a block
         if (row < p.R && whole) {
-          const int hd = h * p.G + row % p.G;
+          const int qi = query_of(p, row), hd = h * p.G + row - qi * p.G;
           const float base = m[i][x] == -INFINITY ? 0.f : m[i][x] * qs[i][x];
           if (p.sinks) sum += ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base);
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
-          uint16_t* dst = p.out + ((static_cast<int64_t>(cur.b) * p.Lq + row / p.G) * p.Hkv * p.G + hd) * D + c0;
+          uint16_t* dst = p.out + ((static_cast<int64_t>(cur.b) * p.Lq + qi) * p.Hkv * p.G + hd) * D + c0;
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k) {
             const float f = ex2(static_cast<float>((E[k] >> 23) - 142)) * inv;
@@ -778,9 +849,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
     if (lane == 0 && opened && !p.whole) {
       const int64_t item = (static_cast<int64_t>(cur.b) * p.Hkv + h) * p.RT + cur.rt;
       p.desc[item] = whole ? make_int4(-1, 0, 0, 0)
-                           : make_int4(static_cast<int>(slot), run, run + (cur.end - 1) / s_per, 0);
+                           : make_int4(static_cast<int>(slot), run, run + (cur.end - 1) / s_per[warp], 0);
     }
-    if (at == cur.end && at < count) cur.next(p);
+    cur = following;
   } while (at < count);
   cp_async_wait<0>();
 }
@@ -870,10 +941,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const K
         for (int c = 0; c < kCols; ++c) v[c] = fmaf(f, s_o[w][kCols * lane + c], v[c]);
       }
     }
-    const int hd = h * p.G + row % p.G;
+    const int qi = query_of(p, row), hd = h * p.G + row - qi * p.G;
     if (p.sinks) sum += ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    uint16_t* dst = p.out + ((static_cast<int64_t>(b) * p.Lq + row / p.G) * p.Hkv * p.G + hd) * D + kCols * lane;
+    uint16_t* dst = p.out + ((static_cast<int64_t>(b) * p.Lq + qi) * p.Hkv * p.G + hd) * D + kCols * lane;
 #pragma unroll
     for (int c = 0; c < kCols; c += 2) *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16(v[c] * inv, v[c + 1] * inv);
   }
@@ -942,6 +1013,7 @@ size_t kv_attention_workspace(int B, int Lq, int Hq, int Hkv, int D, int sms) {
 cudaError_t launch_kv_attention(KvAttentionArgs p, void* workspace, int sms, cudaStream_t st, int* launches) {
   const int nt = tiles_n(p.R);
   p.RT = static_cast<int>(cdiv(p.R, 8 * nt));
+  p.g_reciprocal = static_cast<uint32_t>(((static_cast<uint64_t>(1) << 32) + p.G - 1) / p.G);   // not used for G = 1
   const Layout l = layout(static_cast<int64_t>(p.B) * p.Hkv * p.RT, p.R, p.D, sms);
   char* base = static_cast<char*>(workspace);
   p.desc = reinterpret_cast<int4*>(base + l.desc);

@@ -294,6 +294,7 @@ struct KvAttentionArgs {
   uint16_t* out;                // (B, Lq, Hkv * G, D)
   int* err;
   int RT;                       // row tiles of an item
+  uint32_t g_reciprocal;        // ceil(2^32 / G)
   int whole;                    // 0: items are cut over runs; else warps of one CTA that share an item
   int unit_step;                // keys from a warp's unit of an item to its next
   int4* desc;

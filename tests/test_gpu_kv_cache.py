@@ -210,6 +210,19 @@ def test_attention(B, case):
     assert torch.equal(c.run(B), out)
 
 
+@pytest.mark.parametrize("n", [31, 32, 33, 64, 65, 127, 128, 129, 256, 385])
+@pytest.mark.parametrize("Hq,Hkv,D,Lq", [(5, 1, 64, 1), (14, 2, 128, 1), (6, 2, 64, 7)])
+def test_attention_many_sequences(B, n, Hq, Hkv, D, Lq):
+    """Long runs over many uneven sequences, empty ones and stretches of them among them, so that a
+    warp's first unit can lie in any sequence; groups and row counts that are no power of two."""
+    lens = [0 if i % 7 == 3 or 40 <= i < 75 else 1 + (i * i * 37) % (900 if i % 5 else 40) for i in range(n)]
+    c = Case(B, lens, Lq, Hq, Hkv, D, 16, sinks=True)
+    out = c.run(B)
+    B.mxmoe_check()
+    c.check(out)
+    assert torch.equal(c.run(B), out)
+
+
 def test_attention_scale_strides_and_three_dims(B):
     c = Case(B, [70, 200], 1, 16, 2, 64, 32)
     wide = torch.randn(2, 16 * 64 + 256, device="cuda").bfloat16()
