@@ -6,10 +6,11 @@
 // tensor memory, operands by TMA with 128-byte swizzle, 128 values of K per stage.
 //
 // Two kernels, by how many tiles there are (launch_fp8_linear_fused):
-//  - pair: a persistent CTA pair (cta_group::2) per 256 x 256 tile. Each CTA loads 128 rows of
-//    both operands, so a pair reads 512 rows for 65,536 outputs, a third less from L2 for each
-//    product than a 128 x 256 tile of a single CTA. Two accumulator slots: a tile's epilogue
-//    overlaps the next tile's products.
+//  - pair: a persistent CTA pair (cta_group::2) per tile of 256 tokens by 64 to 256 columns. Each
+//    CTA loads half of either operand's rows, so that a pair reads 512 rows for 65,536 outputs, a
+//    third less from L2 for each product than a 128 x 256 tile of a single CTA. The width is the one
+//    whose rounds over the pairs are the shortest. Two accumulator slots: a tile's epilogue overlaps
+//    the next tile's products.
 //  - split: for few tokens, where the weights' bytes are the bound. Weight rows take the M side
 //    (128 a CTA), tokens the N side (16 to 128), and K is cut over a cluster of up to 8 CTAs
 //    so that every SM streams weights. The partial sums meet through distributed shared
@@ -207,7 +208,7 @@ __device__ __forceinline__ uint4 residual8(const LinearFusedArgs& p, int64_t t, 
 
 // ------------------------------------------------------------------------- pair ----
 namespace pair {
-constexpr int BM = 256, BN = 256;      // of the pair; each CTA loads half of either
+constexpr int BM = 256, kMinBN = 64, kMaxBN = 256;   // of the pair; each CTA loads half of either. Widths are multiples of 32
 constexpr int kStages = 3;
 constexpr int kSub = 2;                // chunks of BK per stage: eight MMAs to a barrier and a commit
 constexpr int kHalf = 128 * BK;        // 16 KB: a CTA's rows of one operand, one chunk
@@ -221,7 +222,7 @@ constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiWarps * kTurn + 256;
 template <int kAct>
 __global__ void __launch_bounds__(pair::kThreads, 1)
 fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
-                       const LinearFusedArgs p) {
+                       const LinearFusedArgs p, const int bn) {
   using namespace pair;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -262,7 +263,7 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
   griddep_launch_dependents();   // only now: a successor's CTA beside this one must not get the tensor memory first
   griddep_wait();
 
-  const int n_tiles = (p.N + BN - 1) / BN, units = ((p.T + BM - 1) / BM) * n_tiles, nk = (p.K + BK - 1) / BK;
+  const int n_tiles = (p.N + bn - 1) / bn, units = ((p.T + BM - 1) / BM) * n_tiles, nk = (p.K + BK - 1) / BK;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (warp == 0) {
@@ -272,12 +273,12 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
       uint32_t phase = 0;
       bool ok = true;
       for (int u = first; u < units && ok; u += step) {
-        const int m0 = (u / n_tiles) * BM + 128 * static_cast<int>(rank), n0 = (u % n_tiles) * BN + 128 * static_cast<int>(rank);
+        const int m0 = (u / n_tiles) * BM + 128 * static_cast<int>(rank), n0 = (u % n_tiles) * bn + bn / 2 * static_cast<int>(rank);
         for (int kt = 0; kt < nk; kt += kSub) {
           if (!mbar_wait_cluster(&empty[stage], phase ^ 1, abort_flag, p.err)) { ok = false; break; }
           const uint32_t bar = peer_addr(smem_u32(&full[stage]), 0);
           const int chunks = min(kSub, nk - kt);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kHalf * chunks);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], (BM + bn) * BK * chunks);
           for (int c = 0; c < chunks; ++c) {
             uint8_t* dst = smem + stage * kStage + 2 * c * kHalf;
             tma_load_2d_pair(dst, &tmap_x, bar, (kt + c) * BK, m0);
@@ -303,13 +304,13 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
     if (rank == 0 && lane == 0) {
       int stage = 0, it = 0;
       uint32_t phase = 0;
-      const uint32_t idesc = idesc_e4m3(BM, BN);
+      const uint32_t idesc = idesc_e4m3(BM, bn);
       const uint64_t desc = smem_desc(smem_u32(smem), 16, 1024, 2);
       bool ok = true, ready = false;
       for (int u = first; u < units && ok; u += step, ++it) {
         const int ab = it & 1;
         if (!mbar_wait_cluster(&acc_empty[ab], ((it >> 1) & 1) ^ 1, abort_flag, p.err)) break;
-        const uint32_t dacc = tmem + ab * BN;
+        const uint32_t dacc = tmem + ab * kMaxBN;
         for (int kt = 0; kt < nk; kt += kSub) {
           if (!ready && !mbar_wait(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
           tc_fence_after();
@@ -337,7 +338,8 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
     // go out (and a residual's come in) per instruction instead of 32 tokens' 16. At 4096 x
     // 2880 -> 5120 the direct stores paced the kernel: 60.1 us against 48.1 without them.
     const int q = warp & 3;              // tensor-memory lane quarter of this warp
-    const int half = (warp - 2) >> 2;    // columns [128 half, 128 half + 128)
+    const int c_split = 32 * ((bn / 32 + 1) / 2);   // four warps take the columns up to it, four the others
+    const int c_first = warp < 6 ? 0 : c_split, c_count = warp < 6 ? c_split : bn - c_split;
     float4* const mine = reinterpret_cast<float4*>(turn + (warp - 2) * kTurn);
     const int row = lane >> 2, col = 8 * (lane & 3);   // the lane's part of a pass: tokens row + 8 i, columns col ..
     // a 32-column chunk's residual, fetched a chunk ahead (from HBM; the column constants, which
@@ -351,21 +353,21 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
     for (int u = first; u < units; u += step, ++it) {
       const int ab = it & 1;
       const int64_t t0 = static_cast<int64_t>(u / n_tiles) * BM + 128 * rank + 32 * q;
-      const int n0 = (u % n_tiles) * BN + 128 * half;
+      const int n0 = (u % n_tiles) * bn + c_first;
       const float sx = t0 + lane < p.T ? (p.sx ? __ldg(p.sx + t0 + lane) * p.s : p.s) : 0.f;
       uint4 res[4], ahead[4];
       fetch(res, t0, n0 + col);
       if (!mbar_wait_cluster(&acc_full[ab], (it >> 1) & 1, abort_flag, p.err)) break;
       __syncwarp();
       tc_fence_after();
-      const uint32_t tbase = tmem + ab * BN + 128 * half + (static_cast<uint32_t>(32 * q) << 16);
+      const uint32_t tbase = tmem + ab * kMaxBN + c_first + (static_cast<uint32_t>(32 * q) << 16);
 #pragma unroll
       for (int c0 = 0; c0 < 128; c0 += 32) {
-        if (n0 + c0 >= p.N || t0 >= p.T) break;
+        if (c0 >= c_count || n0 + c0 >= p.N || t0 >= p.T) break;
         const int n = n0 + c0 + col;
         Columns cols;
         if (n < p.N) cols.load(p, n);
-        if (c0 < 96) fetch(ahead, t0, n + 32);
+        if (c0 + 32 < c_count) fetch(ahead, t0, n + 32);
         uint32_t v[32];
         tc_ld_32x32b_x32(tbase + c0, v);
 #pragma unroll
@@ -582,17 +584,17 @@ bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t K, uin
 }
 
 template <int kAct>
-cudaError_t launch_pair(const LinearFusedArgs& p, int sms, cudaStream_t st) {
+cudaError_t launch_pair(const LinearFusedArgs& p, int bn, int sms, cudaStream_t st) {
   using namespace linf;
   CUtensorMap mx, mw;
-  if (!encode_codes(&mx, p.xq, p.T, p.K, 128) || !encode_codes(&mw, p.wq, p.N, p.K, 128)) return cudaErrorInvalidValue;
+  if (!encode_codes(&mx, p.xq, p.T, p.K, 128) || !encode_codes(&mw, p.wq, p.N, p.K, bn / 2)) return cudaErrorInvalidValue;
   static SmemLimit limit;
   cudaError_t e = limit.raise(fp8_linear_pair_kernel<kAct>, pair::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int64_t units = cdiv(p.T, pair::BM) * cdiv(p.N, pair::BN);
+  const int64_t units = cdiv(p.T, pair::BM) * cdiv(p.N, bn);
   const int grid = 2 * static_cast<int>(std::min<int64_t>(units, sms / 2));
   return launch_early(fp8_linear_pair_kernel<kAct>, dim3(static_cast<unsigned>(grid)), pair::kThreads, pair::kSmemBytes, 2,
-                      st, mx, mw, p);
+                      st, mx, mw, p, bn);
 }
 
 // Clusters of ks CTAs of the split kernel that the device holds at once: a cluster lies in one
@@ -651,24 +653,48 @@ cudaError_t launch_split(const LinearFusedArgs& p, int sms, cudaStream_t st) {
                       split::kThreads, smem, ks, st, mw, mx, p, ks);
 }
 
-// Which kernel for more than 128 tokens: the shorter by what each measured on a B200 over 22 sizes,
-// in units of 10 ns with nk = ceil(K / 128): a round of pairs 1000 + 29 nk (the first; 29 nk each
-// further one), a wave of split CTAs 800 + 42 nk / ks. E.g. 512 x 2880 -> 5120: pairs 19.7 us,
-// split 37.1; 512 x 4096 -> 640: 19.3, 15.0; 200 x 2880 -> 5120: 16.9, 18.6; 200 x 1024 -> 8192: 13.1,
-// 12.4; 4000 x 8192 -> 256: 30.8, 23.8.
-bool pairs_are_shorter(const LinearFusedArgs& p, int sms) {
+// What either kernel takes for more than 64 tokens, in ns, from what they measured on a B200 at 40
+// sizes (64 to 18944 tokens, K 256 to 8192, N 64 to 8192); nk = K / 128 rounded up. Of the widths that
+// were measured at each size the shortest is found at 34 of 34, and of the kernels the shorter at 31
+// of 34 (the others lose up to 9 %).
+//
+// A pair's chunk of K is bound by what one SM draws from L2 (its 128 rows and half of the weights'),
+// and more of it the more SMs draw at once; a narrow tile costs more loads for each product but
+// fills the last round better. E.g. 4096 x 2880 -> 5120: 256 columns 58.0 us, 224 56.7, 160 63.5;
+// 1024 x 2880 -> 5120: 26.9, 25.6, 23.4; 200 x 2880 -> 5120: 256 14.5, 96 12.4; 4000 x 8192 -> 256: 256
+// 28.5, 64 22.7; 777 x 1024 -> 4096: 256 11.2, 128 11.8, 64 14.5.
+int64_t pair_ns(const LinearFusedArgs& p, int bn, int sms) {
   using namespace linf;
-  const int64_t nk = cdiv(p.K, BK);
-  const int64_t rounds = cdiv(cdiv(p.T, pair::BM) * cdiv(p.N, pair::BN), std::max(1, sms / 2));
+  const int64_t nk = cdiv(p.K, BK), pairs = std::max(1, sms / 2);
+  const int64_t tiles = cdiv(p.T, pair::BM) * cdiv(p.N, bn), rounds = cdiv(tiles, pairs);
+  const int64_t chunk = 235 + 30 * bn / 100 + (10 + 53 * bn / 100) * std::min(tiles, pairs) / pairs;
+  return 3200 + 10 * bn + rounds * (500 + std::max<int64_t>(nk * chunk, 1000 + 11 * bn));
+}
+
+int pair_width(const LinearFusedArgs& p, int sms) {
+  using namespace linf;
+  int best = pair::kMaxBN;
+  for (int bn = best - 32; bn >= pair::kMinBN; bn -= 32)
+    if (pair_ns(p, bn, sms) < pair_ns(p, best, sms)) best = bn;
+  return best;
+}
+
+// The split kernel's, 128 tokens wide: a chunk of K each 500, the join 350 for each rank. E.g. (pairs,
+// split) 128 x 512 -> 640: 5.6 us, 7.8; 128 x 8192 -> 1024: 20.4, 13.8; 200 x 2880 -> 5120: 12.2, 18.1;
+// 300 x 8192 -> 1024: 20.6, 14.5; 300 x 4096 -> 4096: 15.1, 22.5.
+int64_t split_ns(const LinearFusedArgs& p, int sms) {
+  using namespace linf;
   const int64_t tiles = cdiv(p.N, split::BM) * cdiv(p.T, 128);
   const int ks = split_ranges<128>(tiles, p.K, sms);
-  const int64_t waves = cdiv(tiles * ks, sms);
-  return 1000 + 29 * nk * rounds < waves * (800 + 42 * nk / ks);
+  return cdiv(tiles * ks, sms) * (6600 + 500 * cdiv(p.K, BK) / ks + 350 * ks);
 }
 
 template <int kAct>
 cudaError_t launch_act(const LinearFusedArgs& p, int sms, cudaStream_t st) {
-  if (p.T > 128 && pairs_are_shorter(p, sms)) return launch_pair<kAct>(p, sms, st);
+  if (p.T > 64) {
+    const int bn = pair_width(p, sms);
+    if (pair_ns(p, bn, sms) < split_ns(p, sms)) return launch_pair<kAct>(p, bn, sms, st);
+  }
   if (p.T <= 16) return launch_split<16, kAct>(p, sms, st);
   if (p.T <= 32) return launch_split<32, kAct>(p, sms, st);
   if (p.T <= 64) return launch_split<64, kAct>(p, sms, st);

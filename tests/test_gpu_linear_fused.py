@@ -72,6 +72,19 @@ def test_linear_fused(B, T, K, N):
         assert torch.equal(B.fp8_linear_fused(c.xq, c.wq, **k), out)
 
 
+@pytest.mark.parametrize("T,K,N", [(66, 96, 40), (100, 32, 136), (250, 480, 8104), (700, 512, 4680), (2300, 64, 1160),
+                                   (1300, 64, 2104), (520, 160, 5000), (260, 512, 13992), (9000, 64, 264), (1100, 96, 3848),
+                                   (5000, 1024, 488), (6000, 1024, 200), (2300, 2048, 904)])
+def test_linear_fused_tile_widths(B, T, K, N):
+    """Sizes whose tiles are 64 to 256 columns wide, the last ones cut, one round of them and several."""
+    c = Case(T, K, N)
+    for k in (dict(s_x=c.sx, s_w=c.sw, bias=c.bias, residual=c.res), dict(s_x=float(c.sx[0]), s_w=c.sw, act="gelu")):
+        out = B.fp8_linear_fused(c.xq, c.wq, **k)
+        B.mxmoe_check()
+        c.check(out, **k)
+        assert torch.equal(B.fp8_linear_fused(c.xq, c.wq, **k), out)
+
+
 @pytest.mark.parametrize("T", [5, 600])
 def test_in_place_residual_and_given_output(B, T):
     c = Case(T, 512, 4096)
