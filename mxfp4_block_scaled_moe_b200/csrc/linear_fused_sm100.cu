@@ -13,8 +13,8 @@
 //    the next tile's products.
 //  - split: for few tokens, where the weights' bytes are the bound. Weight rows take the M side
 //    (128 a CTA), tokens the N side (16 to 128), and K is cut over a cluster of up to 8 CTAs
-//    so that every SM streams weights. The partial sums meet through distributed shared
-//    memory, added in rank order: no workspace, no second launch, the same bits each time.
+//    so that every SM streams weights. The partial sums meet in distributed shared memory,
+//    added in rank order: no workspace, no second launch, the same bits each time.
 //
 // Every mbarrier wait gives up after about a second: the kernel then records MXMOE_ETIMEOUT,
 // lets copies in flight land, meets the rest of its cluster, frees its tensor memory and
@@ -42,20 +42,60 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The issuing warp runs its loop as a whole and predicates these on one elected lane: descriptors and
+// addresses then stay in uniform registers, where the instructions take them from. A loop of one
+// lane moved all of them over before each MMA (92 cycles an MMA, 200 a commit): 1000 x 8192 -> 256,
+// tiles of 64 columns: 20.3 us against 18.2.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+
 template <int kGroup>
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f8(uint32_t elected, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
   if constexpr (kGroup == 1)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
         : "memory");
+}
+
+// arrive on the barrier once the MMAs issued so far are done
+__device__ __forceinline__ void commit(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(elected)
+      : "memory");
+}
+// the same on the barrier at this offset in both CTAs of a pair
+__device__ __forceinline__ void commit_pair(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .b16 m;\n .reg .pred e;\n mov.b16 m, 3;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(elected)
+      : "memory");
+}
+
+// Has the phase completed? Unlike a try_wait, which may hold the warp for microseconds while it has not.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // ------------------------------------------------------------------- cluster -------
@@ -64,22 +104,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
+// The cluster's barrier as a meeting only, without release and acquire: what the CTAs tell each other
+// goes through mbarriers. (Releasing made it wait for the outputs: half a microsecond a call.)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory"); }
 // the address of a shared-memory object of this CTA in the cluster's CTA `rank`
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float4 ld_peer(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+// copies this CTA's shared memory to another's (16-byte pieces), its bytes counted on a barrier there
+__device__ __forceinline__ void send_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
                : "memory");
-  return v;
 }
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
@@ -111,14 +150,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
       "[%2];\n" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-// arrive on the barrier at this offset in both CTAs of the pair once the MMAs issued so far are done
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .b16 m;\n mov.b16 m, 3;\n"
-      " tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
-          smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tc_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -234,7 +265,7 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(acc_empty + 2);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 2) + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform, and known to be
   const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_x)) : "memory");
@@ -257,7 +288,8 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  cluster_arrive();   // the barriers are fenced above, and nothing else is shared yet
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   griddep_launch_dependents();   // only now: a successor's CTA beside this one must not get the tensor memory first
@@ -294,14 +326,13 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
       }
     }
   } else if (warp == 1) {
-    // ------------------------------- MMA issuer (one thread, the leader's) ---------
-    // The tensor pipe takes few MMAs ahead, so this thread's own time shows: an MMA's issue
-    // about 92 cycles (the MMA runs 128), a commit about 200, a fence and a wait on a barrier that
-    // is complete about 80 each. Hence eight MMAs to a stage, the next stage's barrier tried
-    // between them, and descriptors that are one addition. (Per 128 of K, where the MMAs need
-    // 512 cycles: 836 with four MMAs to a stage and the warp waiting before each, 674 with the
-    // early try; no stage was ever late in either.)
-    if (rank == 0 && lane == 0) {
+    // ------------------------------------------- MMA issuer (the leader's warp) ----
+    // What the warp does between MMAs shows, since the tensor pipe takes few ahead: eight MMAs
+    // to a stage and a commit, the next stage's barrier looked at between them, descriptors
+    // that are one addition. (With four MMAs to a stage and a wait before each, 836 cycles for
+    // 128 of K although no stage was late; the MMAs need 512, and this loop takes 525.)
+    if (rank == 0) {
+      const uint32_t elected = elect_one();
       int stage = 0, it = 0;
       uint32_t phase = 0;
       const uint32_t idesc = idesc_e4m3(BM, bn);
@@ -309,10 +340,10 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
       bool ok = true, ready = false;
       for (int u = first; u < units && ok; u += step, ++it) {
         const int ab = it & 1;
-        if (!mbar_wait_cluster(&acc_empty[ab], ((it >> 1) & 1) ^ 1, abort_flag, p.err)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[ab], ((it >> 1) & 1) ^ 1, abort_flag, p.err))) break;
         const uint32_t dacc = tmem + ab * kMaxBN;
         for (int kt = 0; kt < nk; kt += kSub) {
-          if (!ready && !mbar_wait(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
+          if (!ready && !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, p.err))) { ok = false; break; }
           tc_fence_after();
           const uint64_t ad = desc + static_cast<uint64_t>(stage * (kStage / 16)), bd = ad + kHalf / 16;
           uint64_t* const done = &empty[stage];
@@ -321,13 +352,13 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
 #pragma unroll
           for (int kk = 0; kk < 4 * kSub; ++kk) {
             const int at = (kk / 4) * (2 * kHalf / 16) + 2 * (kk % 4);
-            if (kk < steps) mma_f8<2>(dacc, ad + at, bd + at, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
-            if (kk == 4 * kSub - 3) ready = mbar_try_wait(&full[stage], phase);
+            if (kk < steps) mma_f8<2>(elected, dacc, ad + at, bd + at, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+            if (kk == 4 * kSub - 3) ready = __all_sync(0xffffffffu, mbar_test(&full[stage], phase));
           }
-          commit_pair(done);
+          commit_pair(elected, done);
         }
         if (!ok) break;
-        commit_pair(&acc_full[ab]);
+        commit_pair(elected, &acc_full[ab]);
       }
     }
   } else {
@@ -402,7 +433,8 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
     }
   }
   __syncwarp();
-  cluster_sync();      // the other CTA may still signal this one's barriers or read its operands
+  cluster_arrive();
+  cluster_wait();      // the other CTA may still signal this one's barriers or read its operands
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512));
@@ -415,13 +447,26 @@ constexpr int BM = 128;                // weight rows
 constexpr int kThreads = 256;
 constexpr int kMaxK = 8;               // CTAs of a cluster
 constexpr int kA = BM * BK;
+constexpr int kRow = 4 * BM;           // bytes of a token's partial sums
 constexpr int stage_bytes(int BN) { return kA + BN * BK; }
-constexpr int stages(int BN) { return BN <= 64 ? 8 : 6; }
+constexpr int stages(int BN) { return BN <= 64 ? 8 : 5; }
 constexpr int tmem_cols(int BN) { return BN < 32 ? 32 : BN; }
-constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 256; }
+// tokens' sums that a CTA is sent: its share of the tile's tokens from each of the others
+constexpr int recv_rows(int BN) {
+  int most = 0;
+  for (int ks = 2; ks <= kMaxK; ++ks) most = std::max(most, (ks - 1) * ((BN + ks - 1) / ks));
+  return most;
+}
+constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + recv_rows(BN) * kRow + 256; }
+static_assert(smem_bytes(64) <= 232448 && smem_bytes(128) <= 232448, "shared memory of an SM");
 }  // namespace split
 
 // Cluster of ks CTAs: weight rows [128 m, + 128), tokens [BN blockIdx.y, + BN), a K range each.
+// Each CTA owns a share of the tile's tokens: the others send it their sums of those, one bulk
+// copy each, and it adds them and finishes those outputs. Copies cross the cluster at three times
+// the rate of plain loads or stores (26 KB in 0.9 us, 2 us or more), and only the receiver waits:
+// 64 x 4096 -> 2880 took 9.6 us with each CTA loading its share between two barriers, 8.7 with
+// plain stores, and takes 6.3.
 template <int BN, int kAct>
 __global__ void __launch_bounds__(split::kThreads, 1)
 fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
@@ -430,16 +475,21 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
   constexpr int kStages = stages(BN), kStage = stage_bytes(BN);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
+  uint8_t* recv = smem + kStages * kStage;   // [sending rank, this one left out][share][128 weight rows], fp32
+  uint64_t* full = reinterpret_cast<uint64_t*>(recv + recv_rows(BN) * kRow);
   uint64_t* empty = full + kStages;
   uint64_t* done = empty + kStages;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 1);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1) + 1;
+  uint64_t* got = done + 1;                  // the others' sums have arrived
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(got + 1);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(got + 1) + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform, and known to be
   const int rank = static_cast<int>(cluster_rank());
   const int m0 = (blockIdx.x / ks) * BM, t0 = blockIdx.y * BN;
-  const int nk = (p.K + BK - 1) / BK, k0 = rank * nk / ks, k1 = (rank + 1) * nk / ks;
+  const int nk = (p.K + BK - 1) / BK, k0 = rank * nk / ks, count = (rank + 1) * nk / ks - k0;
+  // this CTA's share of the tile's tokens
+  const int tokens = min(BN, p.T - t0), share = (tokens + ks - 1) / ks, mine = rank * share;
+  const int rows = max(0, min(share, tokens - mine));
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_x)) : "memory");
@@ -448,127 +498,149 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
+    mbar_init(got, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    mbar_arrive_expect_tx(got, (ks - 1) * rows * kRow);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tmem_holder)),
                  "r"(tmem_cols(BN)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  griddep_launch_dependents();   // only now: a successor's CTA beside this one must not get the tensor memory first
+  __syncwarp();
+  cluster_arrive();   // this CTA's barriers stand (fenced above): the others may send to it
+  uint32_t tmem = 0;
+  if (warp == 0) {    // needs no tensor memory: the loads start while it is taken
+    asm volatile("bar.arrive 1, %0;\n" ::"n"(kThreads) : "memory");
+  } else {
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;\n" ::"n"(kThreads) : "memory");
+    tc_fence_after();
+    tmem = *tmem_holder;
+    griddep_launch_dependents();   // only now: a successor's CTA beside this one must not get the tensor memory first
+  }
   griddep_wait();
 
   if (warp == 0) {
     if (lane == 0) {
-      for (int kt = k0; kt < k1; ++kt) {
-        const int i = kt - k0, stage = i % kStages;
+      for (int i = 0; i < count; ++i) {
+        const int stage = i % kStages;
         if (i >= kStages && !mbar_wait(&empty[stage], (i / kStages + 1) & 1, abort_flag, p.err)) break;
         mbar_arrive_expect_tx(&full[stage], kStage);
-        tma_load_2d(smem + stage * kStage, &tmap_w, &full[stage], kt * BK, m0);
-        tma_load_2d(smem + stage * kStage + kA, &tmap_x, &full[stage], kt * BK, t0);
+        tma_load_2d(smem + stage * kStage, &tmap_w, &full[stage], (k0 + i) * BK, m0);
+        tma_load_2d(smem + stage * kStage + kA, &tmap_x, &full[stage], (k0 + i) * BK, t0);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint64_t desc = smem_desc(smem_u32(smem), 16, 1024, 2);
-      bool ok = true;
-      for (int kt = k0; kt < k1; ++kt) {
-        const int i = kt - k0, stage = i % kStages;
-        if (!mbar_wait(&full[stage], (i / kStages) & 1, abort_flag, p.err)) { ok = false; break; }
-        tc_fence_after();
-        const uint64_t ad = desc + static_cast<uint64_t>(stage * (kStage / 16)), bd = ad + kA / 16;
-        const int nks = min(4, (p.K - kt * BK) / 32);
-        for (int kk = 0; kk < nks; ++kk)
-          mma_f8<1>(tmem, ad + 2 * kk, bd + 2 * kk, idesc_e4m3(BM, BN), (i > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(&empty[stage]);
+    const uint32_t elected = elect_one();
+    const uint64_t desc = smem_desc(smem_u32(smem), 16, 1024, 2);
+    bool ok = true, ready = false;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < count; ++i) {
+      if (!ready && !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, p.err))) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t ad = desc + static_cast<uint64_t>(stage * (kStage / 16)), bd = ad + kA / 16;
+      uint64_t* const freed = &empty[stage];
+      if (++stage == kStages) { stage = 0; phase ^= 1; }
+      const int steps = min(4, (p.K - (k0 + i) * BK) / 32);   // K % 32 == 0
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (kk < steps) mma_f8<1>(elected, tmem, ad + 2 * kk, bd + 2 * kk, idesc_e4m3(BM, BN), (i > 0 || kk > 0) ? 1u : 0u);
+        if (kk == 2) ready = __all_sync(0xffffffffu, mbar_test(&full[stage], phase));
       }
-      if (ok) tc_commit(done);
+      if (i + kStages < count) commit(elected, freed);   // only a stage that is loaded again
     }
+    if (ok) commit(elected, done);
   }
-  // the cluster's CTAs share the tile's (token, 8 rows) groups; what this thread's first one
-  // needs from global memory is fetched while the products run
-  const int tokens = min(BN, p.T - t0), groups = tokens * (BM / 8);
-  const int g0 = rank * kThreads + threadIdx.x;
+  __syncwarp();
+  // a thread finishes 8 columns, the same for each of its tokens; what they need from global memory is
+  // fetched while the products run
+  constexpr int kPasses = (BN * BM / 8 + kThreads - 1) / kThreads, kStep = kThreads / (BM / 8);
+  const int col = 8 * (threadIdx.x % (BM / 8)), n = m0 + col, row0 = threadIdx.x / (BM / 8);
+  const int passes = n < p.N && row0 < rows ? (rows - row0 + kStep - 1) / kStep : 0;
   Columns cols;
-  uint4 res = make_uint4(0, 0, 0, 0);
-  float sx = 0.f;
-  const auto fetch = [&](int gi) {
-    const int n = m0 + 8 * (gi % (BM / 8));
-    const int64_t t = t0 + gi / (BM / 8);
-    if (gi >= groups || n >= p.N) return;
-    cols.load(p, n);
-    res = residual8(p, t, n);
-    sx = p.sx ? __ldg(p.sx + t) * p.s : p.s;
-  };
-  fetch(g0);
-  // every stage has been consumed when `done` completes: its memory takes the partial sums,
-  // fp32 [token][128 weight rows]
-  float* sums = reinterpret_cast<float*>(smem);
-  if (warp >= 4 && mbar_wait(done, 0, abort_flag, p.err)) {
-    __syncwarp();
-    tc_fence_after();
-    const int q = warp & 3;
-    if constexpr (BN >= 32) {
-      for (int c0 = 0; c0 < BN && t0 + c0 < p.T; c0 += 32) {
-        uint32_t v[32];
-        tc_ld_32x32b_x32(tmem + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
+  uint4 res[kPasses];
+  float sx[kPasses];
+  if (passes > 0) cols.load(p, n);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sums[(c0 + i) * BM + 32 * q + lane] = __uint_as_float(v[i]);
-      }
-    } else {
-      for (int c0 = 0; c0 < BN && t0 + c0 < p.T; c0 += 8) {
-        uint32_t v[8];
-        tc_ld_32x32b_x8(tmem + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
-        tc_wait_ld(v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sums[(c0 + i) * BM + 32 * q + lane] = __uint_as_float(v[i]);
-      }
+  for (int i = 0; i < kPasses; ++i)
+    if (i < passes) {
+      const int64_t t = t0 + mine + row0 + i * kStep;
+      res[i] = residual8(p, t, n);
+      sx[i] = p.sx ? __ldg(p.sx + t) * p.s : p.s;
     }
-    tc_fence_before();
+  __syncwarp();
+  cluster_wait();
+  if (warp == 0) griddep_launch_dependents();   // tensor memory was taken before that barrier
+  // every stage has been consumed when `done` completes: its memory takes this CTA's sums, fp32
+  // [token][128 weight rows]; each share of them is one copy to the share's owner
+  float* const sums = reinterpret_cast<float*>(smem);
+  if (warp >= 4) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, p.err));
+    if (ok) {
+      tc_fence_after();
+      const int q = warp & 3;
+      if constexpr (BN >= 32) {
+        for (int c0 = 0; c0 < tokens; c0 += 32) {
+          uint32_t v[32];
+          tc_ld_32x32b_x32(tmem + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sums[(c0 + i) * BM + 32 * q + lane] = __uint_as_float(v[i]);
+        }
+      } else {
+        for (int c0 = 0; c0 < tokens; c0 += 8) {
+          uint32_t v[8];
+          tc_ld_32x32b_x8(tmem + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
+          tc_wait_ld(v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sums[(c0 + i) * BM + 32 * q + lane] = __uint_as_float(v[i]);
+        }
+      }
+      tc_fence_before();
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    }
+    asm volatile("bar.sync 2, 128;\n" ::: "memory");
+    if (warp == 4 && lane < ks && lane != rank && !*abort_flag) {
+      const int n = min(share, tokens - lane * share);
+      if (n > 0)
+        send_bulk(peer_addr(smem_u32(recv) + (rank < lane ? rank : rank - 1) * share * kRow, lane), sums + lane * share * BM,
+                  n * kRow, peer_addr(smem_u32(got), lane));
+    }
   }
-  __syncthreads();
+  __syncthreads();     // this CTA's own sums; the accumulators have been read
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(tmem_cols(BN)));
+  }
+  const bool whole = mbar_wait_cluster(got, 0, abort_flag, p.err);
+  __syncwarp();
+  cluster_arrive();   // what was sent to this CTA is here
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i)
+    if (whole && i < passes) {
+      const int row = row0 + i * kStep, at = 4 * (row * BM + col);
+      float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < kMaxK; ++r)
+        if (r < ks) {              // added in rank order
+          const uint8_t* from = (r == rank ? smem + mine * kRow : recv + (r < rank ? r : r - 1) * share * kRow) + at;
+          const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 16);
+          a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+          a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+        }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) a[c] *= sx[i];
+      finish8<kAct>(p, t0 + mine + row, n, a, cols, res[i]);
+    }
   if (*abort_flag) {   // let copies already issued land before the CTA's shared memory goes
     const long long c0 = clock64();
     while (clock64() - c0 < 200000) {
     }
   }
   __syncwarp();
-  cluster_sync();
-  const uint32_t base = smem_u32(sums);
-  for (int gi = g0; gi < groups; gi += ks * kThreads) {
-    const int tok = gi / (BM / 8), n = m0 + 8 * (gi % (BM / 8));
-    if (gi != g0) fetch(gi);
-    if (n >= p.N) continue;
-    float4 x[kMaxK], y[kMaxK];   // all ranks' sums on their way at once
-#pragma unroll
-    for (int r = 0; r < kMaxK; ++r)
-      if (r < ks) {
-        const uint32_t at = peer_addr(base + 4 * (tok * BM + 8 * (gi % (BM / 8))), r);
-        x[r] = ld_peer(at);
-        y[r] = ld_peer(at + 16);
-      }
-    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int r = 0; r < kMaxK; ++r)
-      if (r < ks) {              // added in rank order
-        a[0] += x[r].x; a[1] += x[r].y; a[2] += x[r].z; a[3] += x[r].w;
-        a[4] += y[r].x; a[5] += y[r].y; a[6] += y[r].z; a[7] += y[r].w;
-      }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] *= sx;
-    finish8<kAct>(p, t0 + tok, n, a, cols, res);
-  }
-  __syncwarp();
-  cluster_sync();      // this CTA's sums have been read
-  if (warp == 1) {
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(tmem_cols(BN)));
-  }
+  cluster_wait();      // what this CTA sent has been received
 }
 
 }  // namespace linf
@@ -654,15 +726,13 @@ cudaError_t launch_split(const LinearFusedArgs& p, int sms, cudaStream_t st) {
 }
 
 // What either kernel takes for more than 64 tokens, in ns, from what they measured on a B200 at 40
-// sizes (64 to 18944 tokens, K 256 to 8192, N 64 to 8192); nk = K / 128 rounded up. Of the widths that
-// were measured at each size the shortest is found at 34 of 34, and of the kernels the shorter at 31
-// of 34 (the others lose up to 9 %).
+// sizes (65 to 18944 tokens, K 64 to 8192, N 64 to 8192); nk = K / 128 rounded up.
 //
 // A pair's chunk of K is bound by what one SM draws from L2 (its 128 rows and half of the weights'),
 // and more of it the more SMs draw at once; a narrow tile costs more loads for each product but
-// fills the last round better. E.g. 4096 x 2880 -> 5120: 256 columns 58.0 us, 224 56.7, 160 63.5;
-// 1024 x 2880 -> 5120: 26.9, 25.6, 23.4; 200 x 2880 -> 5120: 256 14.5, 96 12.4; 4000 x 8192 -> 256: 256
-// 28.5, 64 22.7; 777 x 1024 -> 4096: 256 11.2, 128 11.8, 64 14.5.
+// fills the last round better. E.g. 4096 x 2880 -> 5120: 256 columns 57.8 us, 224 55.4, 160 62.8;
+// 1024 x 2880 -> 5120: 160 22.2, 256 26.3, 64 36.9; 200 x 2880 -> 5120: 96 11.1, 256 14.5; 1000 x 8192 ->
+// 256: 64 17.9, 160 19.9, 256 25.7; 777 x 1024 -> 4096: 256 11.1, 128 11.8, 64 13.9.
 int64_t pair_ns(const LinearFusedArgs& p, int bn, int sms) {
   using namespace linf;
   const int64_t nk = cdiv(p.K, BK), pairs = std::max(1, sms / 2);
@@ -679,14 +749,15 @@ int pair_width(const LinearFusedArgs& p, int sms) {
   return best;
 }
 
-// The split kernel's, 128 tokens wide: a chunk of K each 500, the join 350 for each rank. E.g. (pairs,
-// split) 128 x 512 -> 640: 5.6 us, 7.8; 128 x 8192 -> 1024: 20.4, 13.8; 200 x 2880 -> 5120: 12.2, 18.1;
-// 300 x 8192 -> 1024: 20.6, 14.5; 300 x 4096 -> 4096: 15.1, 22.5.
+// The split kernel's, 128 tokens wide. E.g. (pairs, split) 128 x 512 -> 640: 5.6 us, 6.3; 128 x 1024 ->
+// 8192: 8.4, 7.6; 128 x 8192 -> 1024: 17.9, 9.7; 200 x 2880 -> 5120: 11.1, 15.2; 300 x 8192 -> 1024: 18.3,
+// 11.3; 300 x 4096 -> 4096: 13.9, 18.4; 4000 x 8192 -> 256: 22.0, 17.9. Up to 64 tokens its tiles are
+// narrower and it is the shorter everywhere (64 x 1024 -> 8192: 7.8, 5.6; 64 x 512 -> 640: 4.9, 4.9).
 int64_t split_ns(const LinearFusedArgs& p, int sms) {
   using namespace linf;
   const int64_t tiles = cdiv(p.N, split::BM) * cdiv(p.T, 128);
   const int ks = split_ranges<128>(tiles, p.K, sms);
-  return cdiv(tiles * ks, sms) * (6600 + 500 * cdiv(p.K, BK) / ks + 350 * ks);
+  return cdiv(tiles * ks, sms) * (6000 + 370 * cdiv(p.K, BK) / ks);
 }
 
 template <int kAct>
