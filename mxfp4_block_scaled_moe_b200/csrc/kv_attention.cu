@@ -101,31 +101,6 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// pairs of fp32: one instruction for both halves, half the issue slots of the scalar forms
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float lo_of(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi_of(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -621,18 +596,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
             uint32_t a[4], b[4];
             expand(w[2 * kk], a);
             expand(w[2 * kk + 1], b);
-            const f32x2 f0 = kk ? pair(ka.y, ka.y) : pair(ka.x, ka.x), f1 = kk ? pair(kb.y, kb.y) : pair(kb.x, kb.x);
+            const f32x2 f0 = kk ? f32x2_of(ka.y, ka.y) : f32x2_of(ka.x, ka.x), f1 = kk ? f32x2_of(kb.y, kb.y) : f32x2_of(kb.x, kb.x);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
               float c[4];
               mma_f16_zero(c, a[0], b[0], a[1], b[1], qf[i][k][0], qf[i][k][1]);
               mma_f16(c, a[2], b[2], a[3], b[3], qf[i][k][2], qf[i][k][3]);
               if (k == 0) {
-                s[i][y][0] = mul2(pair(c[0], c[1]), f0);
-                s[i][y][1] = mul2(pair(c[2], c[3]), f1);
+                s[i][y][0] = mul2(f32x2_of(c[0], c[1]), f0);
+                s[i][y][1] = mul2(f32x2_of(c[2], c[3]), f1);
               } else {
-                s[i][y][0] = fma2(pair(c[0], c[1]), f0, s[i][y][0]);
-                s[i][y][1] = fma2(pair(c[2], c[3]), f1, s[i][y][1]);
+                s[i][y][0] = fma2(f32x2_of(c[0], c[1]), f0, s[i][y][0]);
+                s[i][y][1] = fma2(f32x2_of(c[2], c[3]), f1, s[i][y][1]);
               }
             }
           }
@@ -654,7 +629,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
             for (int z = 0; z < 2; ++z) {
               const int key = key0 + 16 * y + 8 * z + g;
               const bool gone = !((pages >> y) & 1);
-              s[i][y][z] = pair(gone || key < lo[0] || key >= hi[0] ? -INFINITY : lo_of(s[i][y][z]),
+              s[i][y][z] = f32x2_of(gone || key < lo[0] || key >= hi[0] ? -INFINITY : lo_of(s[i][y][z]),
                                 gone || key < lo[1] || key >= hi[1] ? -INFINITY : hi_of(s[i][y][z]));
             }
         }
@@ -698,15 +673,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
       }
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const f32x2 base = pair(m[i][0] == -INFINITY ? 0.f : -m[i][0], m[i][1] == -INFINITY ? 0.f : -m[i][1]);
-        const f32x2 q2 = pair(qs[i][0], qs[i][1]);
-        f32x2 sum = pair(l[i][0], l[i][1]);
+        const f32x2 base = f32x2_of(m[i][0] == -INFINITY ? 0.f : -m[i][0], m[i][1] == -INFINITY ? 0.f : -m[i][1]);
+        const f32x2 q2 = f32x2_of(qs[i][0], qs[i][1]);
+        f32x2 sum = f32x2_of(l[i][0], l[i][1]);
 #pragma unroll
         for (int y = 0; y < S::kTiles; ++y)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             const f32x2 e = mul2(add2(s[i][y][z], base), q2);
-            s[i][y][z] = pair(ex2(lo_of(e)), ex2(hi_of(e)));
+            s[i][y][z] = f32x2_of(ex2(lo_of(e)), ex2(hi_of(e)));
             sum = add2(sum, s[i][y][z]);
           }
         l[i][0] = lo_of(sum);
@@ -734,7 +709,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
             uint32_t ae[4], ao[4];
             expand(even, ae);
             expand(odd, ao);
-            const f32x2 f0 = kk ? pair(va.y, va.y) : pair(va.x, va.x), f1 = kk ? pair(vb.y, vb.y) : pair(vb.x, vb.x);
+            const f32x2 f0 = kk ? f32x2_of(va.y, va.y) : f32x2_of(va.x, va.x), f1 = kk ? f32x2_of(vb.y, vb.y) : f32x2_of(vb.x, vb.x);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
               const f32x2 wa = mul2(s[i][y][0], f0), wb = mul2(s[i][y][1], f1);

@@ -120,8 +120,9 @@ __device__ __forceinline__ void send_bulk(uint32_t dst, const void* src, uint32_
                "r"(smem_u32(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
+// relaxed: it tells of tensor memory that has been read (and waited for), and is not to wait for the outputs
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
 }
 // mbar_wait with cluster scope: some of the barrier's arrivals come from the other CTA
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
@@ -166,75 +167,88 @@ __device__ __forceinline__ void tc_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[3
 }
 
 // ------------------------------------------------------------------- epilogue ------
-// erfc(x) = e^{-x^2} sum_i c_i t^i, t = 1 / (1 + x / 2), for x >= 0: the coefficients are a
-// weighted least-squares fit made for this file, relative error below 1.4e-6 on [0, 10]
-// (scaled complementary error functions are smooth in such a t). About 15 instructions; the
-// library's erfcf made the epilogue the bound (21 us for 777 x 1024 x 4096).
-__device__ __forceinline__ float half_erfc(float x) {
-  float t, e;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.5f, x, 1.0f)));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * x * -1.44269504088896f));
-  float s = 8.820403348e-02f;
-  s = fmaf(s, t, -3.567371556e-01f);
-  s = fmaf(s, t, 3.892230589e-01f);
-  s = fmaf(s, t, 3.789172870e-02f);
-  s = fmaf(s, t, 2.815033596e-01f);
-  s = fmaf(s, t, 2.775822159e-01f);
-  s = fmaf(s, t, 2.823314067e-01f);
-  return 0.5f * s * t * e;
+__device__ __forceinline__ f32x2 both(float v) { return f32x2_of(v, v); }
+__device__ __forceinline__ f32x2 rcp2(f32x2 v) {
+  float a, b;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(lo_of(v)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(hi_of(v)));
+  return f32x2_of(a, b);
+}
+__device__ __forceinline__ f32x2 exp2_2(f32x2 v) {
+  float a, b;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(lo_of(v)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(hi_of(v)));
+  return f32x2_of(a, b);
 }
 
+// Activations of two values. GELU is max(v, 0) - |v| erfc(x) / 2 with x = |v| / sqrt(2), and
+// erfc(x) / 2 = e^{-x^2} sum_i c_i t^i, t = 1 / (1 + x / 2): the coefficients are half of a
+// weighted least-squares fit made for this file, relative error below 1.4e-6 on [0, 10] (scaled
+// complementary error functions are smooth in such a t). Beyond |v| = 30 it is 0 in fp32, so |v|
+// stops there and infinities pass. 777 x 1024 -> 4096: 12.4 us by single values, 11.3 by pairs; the
+// library's erfcf took 21.
 template <int kAct>
-__device__ __forceinline__ float activate(float v) {
-  if constexpr (kAct == MXMOE_ACT_SILU) return __fdividef(v, 1.0f + __expf(-v));
+__device__ __forceinline__ f32x2 activate(f32x2 v) {
+  if constexpr (kAct == MXMOE_ACT_SILU)
+    return mul2(v, rcp2(add2(exp2_2(mul2(v, both(-1.44269504088896f))), both(1.f))));
   if constexpr (kAct == MXMOE_ACT_GELU) {
-    const float h = half_erfc(fabsf(v) * 0.70710678118654752f);
-    return v * (v < 0.0f ? h : 1.0f - h);
+    const f32x2 a = f32x2_of(fmaxf(-fabsf(lo_of(v)), -30.f), fmaxf(-fabsf(hi_of(v)), -30.f));   // -|v|
+    const f32x2 t = rcp2(fma2(a, both(-0.35355339059327f), both(1.f)));
+    const f32x2 e = exp2_2(mul2(mul2(v, v), both(-0.72134752044448f)));
+    f32x2 s = both(4.4102016e-02f);
+    s = fma2(s, t, both(-1.7836859e-01f));
+    s = fma2(s, t, both(1.9461153e-01f));
+    s = fma2(s, t, both(1.8945863e-02f));
+    s = fma2(s, t, both(1.4075167e-01f));
+    s = fma2(s, t, both(1.3879111e-01f));
+    s = fma2(s, t, both(1.4116570e-01f));
+    return fma2(a, mul2(mul2(s, t), e), f32x2_of(fmaxf(lo_of(v), 0.f), fmaxf(hi_of(v), 0.f)));
   }
   return v;
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ uint32_t pack2(f32x2 v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo_of(v), hi_of(v));
+  return *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // What eight columns [n, n + 8) share over the tokens: channel scales and bias.
 struct Columns {
-  float w[8], b[8];
+  f32x2 w[4], b[4];
   __device__ __forceinline__ void load(const LinearFusedArgs& p, int n) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = 1.f;
-      b[i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      w[i] = both(1.f);
+      b[i] = 0;
     }
     if (p.sw) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(p.sw + n)), y = __ldg(reinterpret_cast<const float4*>(p.sw + n) + 1);
-      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w; w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+      const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2*>(p.sw + n)), y = __ldg(reinterpret_cast<const ulonglong2*>(p.sw + n) + 1);
+      w[0] = x.x; w[1] = x.y; w[2] = y.x; w[3] = y.y;
     }
     if (p.bias) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(p.bias + n)), y = __ldg(reinterpret_cast<const float4*>(p.bias + n) + 1);
-      b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w; b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
+      const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2*>(p.bias + n)), y = __ldg(reinterpret_cast<const ulonglong2*>(p.bias + n) + 1);
+      b[0] = x.x; b[1] = x.y; b[2] = y.x; b[3] = y.y;
     }
   }
 };
 
-// Those columns' outputs of token t, from their sums times the token's scale; r: their residual
+// Those columns' outputs of a token, from element `at` of the output on, from their sums times the
+// token's scale; r: their residual
 // (zeros without one, which add nothing but turn a -0 into +0).
 template <int kAct>
-__device__ __forceinline__ void finish8(const LinearFusedArgs& p, int64_t t, int n, const float (&acc)[8],
-                                        const Columns& c, const uint4& r) {
+__device__ __forceinline__ void finish8(const LinearFusedArgs& p, int64_t at, const f32x2 (&acc)[4], const Columns& c,
+                                        const uint4& r) {
   const uint32_t ru[4] = {r.x, r.y, r.z, r.w};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    o[i] = pack2(activate<kAct>(fmaf(acc[2 * i], c.w[2 * i], c.b[2 * i])) + __uint_as_float(ru[i] << 16),
-                 activate<kAct>(fmaf(acc[2 * i + 1], c.w[2 * i + 1], c.b[2 * i + 1])) + __uint_as_float(ru[i] & 0xFFFF0000u));
-  *reinterpret_cast<uint4*>(p.out + t * p.N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+    o[i] = pack2(add2(activate<kAct>(fma2(acc[i], c.w[i], c.b[i])),
+                      f32x2_of(__uint_as_float(ru[i] << 16), __uint_as_float(ru[i] & 0xFFFF0000u))));
+  *reinterpret_cast<uint4*>(p.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-__device__ __forceinline__ uint4 residual8(const LinearFusedArgs& p, int64_t t, int n) {
-  return p.residual ? *reinterpret_cast<const uint4*>(p.residual + t * p.N + n) : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ uint4 residual8(const LinearFusedArgs& p, int64_t at) {
+  return p.residual ? *reinterpret_cast<const uint4*>(p.residual + at) : make_uint4(0, 0, 0, 0);
 }
 
 // ------------------------------------------------------------------------- pair ----
@@ -371,14 +385,13 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
     const int q = warp & 3;              // tensor-memory lane quarter of this warp
     const int c_split = 32 * ((bn / 32 + 1) / 2);   // four warps take the columns up to it, four the others
     const int c_first = warp < 6 ? 0 : c_split, c_count = warp < 6 ? c_split : bn - c_split;
-    float4* const mine = reinterpret_cast<float4*>(turn + (warp - 2) * kTurn);
+    ulonglong2* const mine = reinterpret_cast<ulonglong2*>(turn + (warp - 2) * kTurn);
     const int row = lane >> 2, col = 8 * (lane & 3);   // the lane's part of a pass: tokens row + 8 i, columns col ..
-    // a 32-column chunk's residual, fetched a chunk ahead (from HBM; the column constants, which
-    // every token tile reads again, come from L1 or L2)
-    const auto fetch = [&](uint4 (&res)[4], int64_t t0, int n) {
+    // a 32-column chunk's residual and column constants are fetched a chunk ahead
+    const int64_t down = 8 * static_cast<int64_t>(p.N);   // eight tokens further
+    const auto fetch = [&](uint4 (&res)[4], int64_t at, int left, bool in) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)   // N % 8 == 0: a group of 8 columns is wholly in or out
-        res[i] = n < p.N && t0 + row + 8 * i < p.T ? residual8(p, t0 + row + 8 * i, n) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i) res[i] = in && 8 * i < left ? residual8(p, at + i * down) : make_uint4(0, 0, 0, 0);
     };
     int it = 0;
     for (int u = first; u < units; u += step, ++it) {
@@ -386,8 +399,13 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
       const int64_t t0 = static_cast<int64_t>(u / n_tiles) * BM + 128 * rank + 32 * q;
       const int n0 = (u % n_tiles) * bn + c_first;
       const float sx = t0 + lane < p.T ? (p.sx ? __ldg(p.sx + t0 + lane) * p.s : p.s) : 0.f;
-      uint4 res[4], ahead[4];
-      fetch(res, t0, n0 + col);
+      uint4 res[4], res_ahead[4];
+      Columns cols, cols_ahead;
+      // the lane's first element, and how many tokens are left from it on
+      const int64_t at0 = (t0 + row) * p.N + n0 + col;
+      const int left = static_cast<int>(min(static_cast<int64_t>(32), p.T - t0 - row));
+      fetch(res, at0, left, n0 + col < p.N);   // N % 8 == 0: a group of 8 columns is wholly in or out
+      if (n0 + col < p.N) cols.load(p, n0 + col);
       if (!mbar_wait_cluster(&acc_full[ab], (it >> 1) & 1, abort_flag, p.err)) break;
       __syncwarp();
       tc_fence_after();
@@ -396,27 +414,30 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
       for (int c0 = 0; c0 < 128; c0 += 32) {
         if (c0 >= c_count || n0 + c0 >= p.N || t0 >= p.T) break;
         const int n = n0 + c0 + col;
-        Columns cols;
-        if (n < p.N) cols.load(p, n);
-        if (c0 + 32 < c_count) fetch(ahead, t0, n + 32);
+        if (c0 + 32 < c_count) {
+          fetch(res_ahead, at0 + c0 + 32, left, n + 32 < p.N);
+          if (n + 32 < p.N) cols_ahead.load(p, n + 32);
+        }
         uint32_t v[32];
         tc_ld_32x32b_x32(tbase + c0, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          mine[8 * lane + (j ^ (lane & 7))] =
-              make_float4(__uint_as_float(v[4 * j]) * sx, __uint_as_float(v[4 * j + 1]) * sx,
-                          __uint_as_float(v[4 * j + 2]) * sx, __uint_as_float(v[4 * j + 3]) * sx);
+        for (int j = 0; j < 8; ++j) {
+          const f32x2 x = mul2(f32x2_of(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), both(sx));
+          const f32x2 y = mul2(f32x2_of(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), both(sx));
+          mine[8 * lane + (j ^ (lane & 7))] = make_ulonglong2(x, y);
+        }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = row + 8 * i;
-          const float4 x = mine[8 * r + ((col / 4) ^ (r & 7))], y = mine[8 * r + ((col / 4 + 1) ^ (r & 7))];
-          const float a[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          if (n < p.N && t0 + r < p.T) finish8<kAct>(p, t0 + r, n, a, cols, res[i]);
+          const ulonglong2 x = mine[8 * r + ((col / 4) ^ (r & 7))], y = mine[8 * r + ((col / 4 + 1) ^ (r & 7))];
+          const f32x2 a[4] = {x.x, x.y, y.x, y.y};
+          if (n < p.N && 8 * i < left) finish8<kAct>(p, at0 + c0 + i * down, a, cols, res[i]);
         }
         __syncwarp();
+        cols = cols_ahead;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) res[i] = ahead[i];
+        for (int i = 0; i < 4; ++i) res[i] = res_ahead[i];
       }
       tc_fence_before();
       __syncwarp();
@@ -568,7 +589,7 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
   for (int i = 0; i < kPasses; ++i)
     if (i < passes) {
       const int64_t t = t0 + mine + row0 + i * kStep;
-      res[i] = residual8(p, t, n);
+      res[i] = residual8(p, t * p.N + n);
       sx[i] = p.sx ? __ldg(p.sx + t) * p.s : p.s;
     }
   __syncwarp();
@@ -621,18 +642,17 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
   for (int i = 0; i < kPasses; ++i)
     if (whole && i < passes) {
       const int row = row0 + i * kStep, at = 4 * (row * BM + col);
-      float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      f32x2 a[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int r = 0; r < kMaxK; ++r)
         if (r < ks) {              // added in rank order
           const uint8_t* from = (r == rank ? smem + mine * kRow : recv + (r < rank ? r : r - 1) * share * kRow) + at;
-          const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 16);
-          a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
-          a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(from), y = *reinterpret_cast<const ulonglong2*>(from + 16);
+          a[0] = add2(a[0], x.x); a[1] = add2(a[1], x.y); a[2] = add2(a[2], y.x); a[3] = add2(a[3], y.y);
         }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) a[c] *= sx[i];
-      finish8<kAct>(p, t0 + mine + row, n, a, cols, res[i]);
+      for (int c = 0; c < 4; ++c) a[c] = mul2(a[c], both(sx[i]));
+      finish8<kAct>(p, static_cast<int64_t>(t0 + mine + row) * p.N + n, a, cols, res[i]);
     }
   if (*abort_flag) {   // let copies already issued land before the CTA's shared memory goes
     const long long c0 = clock64();
