@@ -22,7 +22,7 @@
 namespace mxmoe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 __device__ __forceinline__ void quantize8(const uint4& v, uint32_t& codes, uint32_t& scale) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -98,8 +98,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(KvAppendArgs p, int
 }  // namespace
 
 // Tokens per CTA: as many as give each of its threads its two pieces, fewer where that would leave
-// SMs idle. 16384 tokens of 8 heads
-// of 64 (42.5 MB): 10.3 us, 4.1 TB/s; with twice the tokens a CTA 10.8, one token a CTA 12.3.
+// SMs idle. 16384 tokens of 8 heads of 64 (42.5 MB), slices of a fused projection: 9.7 us, 4.4 TB/s;
+// 1024 tokens 2.9. With 256 threads a CTA 10.4 and 3.5, 512 11.1 and 4.8, 64 11.0 and 2.9; one piece a
+// thread 10.9 and 2.2, four 10.4 and 3.6.
 cudaError_t launch_kv_append(const KvAppendArgs& p, int sms, cudaStream_t st) {
   const int vecs = p.Hkv * (p.D / 8);
   int shift = 0;
