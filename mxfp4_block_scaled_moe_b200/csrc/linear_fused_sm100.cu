@@ -354,7 +354,8 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
       bool ok = true, ready = false;
       for (int u = first; u < units && ok; u += step, ++it) {
         const int ab = it & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[ab], ((it >> 1) & 1) ^ 1, abort_flag, p.err))) break;
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[ab], ((it >> 1) & 1) ^ 1, abort_flag, p.err));
+        if (!ok) break;
         const uint32_t dacc = tmem + ab * kMaxBN;
         for (int kt = 0; kt < nk; kt += kSub) {
           if (!ready && !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, p.err))) { ok = false; break; }
@@ -374,6 +375,9 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
         if (!ok) break;
         commit_pair(elected, &acc_full[ab]);
       }
+      // the other CTA's last signals have reached this CTA's barriers before it leaves
+      for (int j = max(0, it - 2); ok && j < it; ++j)
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[j & 1], (j >> 1) & 1, abort_flag, p.err));
     }
   } else {
     // --------------------------------------------------------------- epilogue -----
