@@ -29,13 +29,13 @@
 // one CTA. Nothing in the result depends on timing, and no counter outlives a call.
 //
 // Measured on a B200 (time, of the bytes that must be read): 64 sequences of 500 to 8192 keys, 64
-// heads over 8 of 64 (154 MB): 49.3 us, 3.1 TB/s; 3 sequences of up to 131072 keys, 2 queries each,
-// 32 heads over 8 of 128 (318 MB): 81.5 us, 3.9 TB/s; one query over a window of 128: 5.6 us. Of
+// heads over 8 of 64 (154 MB): 44.9 us, 3.4 TB/s; 3 sequences of up to 131072 keys, 2 queries each,
+// 32 heads over 8 of 128 (318 MB): 78.6 us, 4.0 TB/s; one query over a window of 128: 4.8 us. Of
 // the first, about 9 us are launches, the start's chain of loads (lengths, table, keys) and the
-// joining kernel; without the products the stream takes 30 us more, without the stream the
-// products 36. The products are paced by the integer pipe (code expansion, 64 lanes a cycle:
-// half of the cycles) and the matrix instructions, which on this part take issue slots from
-// it (an m16n8k16 between such instructions costs about 5 cycles beyond its own 8).
+// joining kernel. The products are paced by the integer pipe (code expansion, 64 lanes a cycle:
+// half of the cycles), the matrix instructions, which on this part take issue slots from it (an
+// m16n8k16 between such instructions costs about 5 cycles beyond its own 8), and by latency: twelve
+// warps issue in half of the cycles, and more do not fit the registers.
 #include <algorithm>
 
 #include "common.cuh"
@@ -519,6 +519,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
       const uint8_t* sk = ring + stage * S::kStageBytes;
       const uint32_t sk_at = ring_at + stage * S::kStageBytes;
       const uint8_t *ssk = sk + 2 * S::kKV, *ssv = ssk + S::kSc;
+      // the unit's key codes and scales are on their way while the next unit's copies are issued (each
+      // read just before its use: 46.1 and 81.0 us instead of 44.9 and 78.6, 64 heads of 64, 32 of 128)
+      uint32_t kw[S::kTiles][S::kBlocks / 2][4];
+#pragma unroll
+      for (int y = 0; y < S::kTiles; ++y)
+#pragma unroll
+        for (int k2 = 0; k2 < S::kBlocks; k2 += 2) ldmatrix(sk_at + (get ^ (16 * k2)) + 16 * y * S::kRowBytes, kw[y][k2 / 2]);
+      uint32_t sc[S::kUnit / 32], ev[S::kUnit / 32];
+#pragma unroll
+      for (int e = 0; e < S::kUnit / 32; ++e) {
+        sc[e] = lds_scales<S::kBlocks>(ssk + (32 * e + lane) * S::kBlocks);
+        ev[e] = lds_scales<S::kBlocks>(ssv + (32 * e + lane) * S::kBlocks);
+      }
       {
         const int next = stage + S::kStages - 1;
         issue(next >= S::kStages ? next - S::kStages : next);
@@ -531,12 +544,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
       // lane takes keys lane (and lane + 32). A key that no row sees counts as scale 0: what
       // lies in its place does not matter.
       const bool edge = pages != (1u << S::kTiles) - 1 || key0 < full_lo || key0 + S::kUnit > full_hi;
-      uint32_t sc[S::kUnit / 32], ev[S::kUnit / 32], top[S::kBlocks];
+      uint32_t top[S::kBlocks];
+      if (edge) {
 #pragma unroll
-      for (int e = 0; e < S::kUnit / 32; ++e) {
-        sc[e] = lds_scales<S::kBlocks>(ssk + (32 * e + lane) * S::kBlocks);
-        ev[e] = lds_scales<S::kBlocks>(ssv + (32 * e + lane) * S::kBlocks);
-        if (edge) {
+        for (int e = 0; e < S::kUnit / 32; ++e) {
           const int key = key0 + 32 * e + lane;
           if (key < seen_lo || key >= seen_hi || !((pages >> (2 * e + (lane >> 4))) & 1)) ev[e] = 0;
         }
@@ -587,8 +598,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
         const float* fb = fa + 8 * 2 * S::kBlocks;
 #pragma unroll
         for (int k2 = 0; k2 < S::kBlocks; k2 += 2) {
-          uint32_t w[4];
-          ldmatrix(sk_at + (get ^ (16 * k2)) + 16 * y * S::kRowBytes, w);
+          const uint32_t(&w)[4] = kw[y][k2 / 2];
           const float2 ka = *reinterpret_cast<const float2*>(fa + k2), kb = *reinterpret_cast<const float2*>(fb + k2);
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk) {
