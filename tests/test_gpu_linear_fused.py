@@ -154,3 +154,23 @@ def test_refusals(B):
             bad()
         assert ei.value.rc == rc
     assert B.fp8_linear_fused(c.xq[:0], c.wq, 1.0, 1.0).shape == (0, 32)
+
+
+@pytest.mark.parametrize("T,N", [(1, 4096), (40, 4096), (300, 4096)])   # either kernel
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_linear_fused_activation_range(B, T, N, act):
+    """The activations over their whole range, given by the bias over codes of zero. A bf16 rounding
+    (2^-8), and 2^-14 for the functions: their exponent is at most 2^7 and is rounded to 2^-23 of it
+    by two steps, the fit adds 2^-19. Below 87.4 2^-126 the reciprocal of 1 + e^-v is flushed."""
+    v = torch.cat((torch.linspace(-16, 16, 3001), torch.linspace(-200, 200, 1001),
+                   torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-3, -1e-3, 1e4, -1e4, 1e30, -1e30, 3e38, -3e38]))).float()
+    v = torch.cat((v, torch.zeros(N - v.numel()))).cuda()
+    xq, wq = (torch.zeros(n, 64, dtype=torch.uint8, device="cuda") for n in (T, N))
+    out = B.fp8_linear_fused(xq, wq, 1.0, 1.0, bias=v, act=act).double()
+    d = v.double()
+    y = d * torch.sigmoid(d) if act == "silu" else d * 0.5 * torch.special.erfc(-d / 2 ** 0.5)
+    assert bool(((out - y).abs() <= y.abs() * (2.0 ** -8 + 2.0 ** -14) + 87.4 * 2.0 ** -126).all())
+    big = torch.full((N,), float("inf"), device="cuda")
+    assert bool(B.fp8_linear_fused(xq, wq, 1.0, 1.0, bias=big, act=act).isinf().all())
+    assert bool(B.fp8_linear_fused(xq, wq, 1.0, 1.0, bias=big * 0, act=act).isnan().all())
+    B.mxmoe_check()
