@@ -385,7 +385,9 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
     // side. Each warp turns 32 x 32 sums through its own buffer (16-byte pieces permuted by
     // the token, so that both sides are free of bank conflicts): then eight tokens' 64 bytes
     // go out (and a residual's come in) per instruction instead of 32 tokens' 16. At 4096 x
-    // 2880 -> 5120 the direct stores paced the kernel: 60.1 us against 48.1 without them.
+    // 2880 -> 5120 the direct stores paced the kernel: 60.1 us against 48.1 without them. Steps of 16
+    // columns let twelve or sixteen warps fit, but took 52.1 and 54.4 us (eight 51.6) against 50.4;
+    // 16 tokens by 64 columns 53.6.
     const int q = warp & 3;              // tensor-memory lane quarter of this warp
     const int c_split = 32 * ((bn / 32 + 1) / 2);   // four warps take the columns up to it, four the others
     const int c_first = warp < 6 ? 0 : c_split, c_count = warp < 6 ? c_split : bn - c_split;
