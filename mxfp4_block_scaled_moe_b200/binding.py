@@ -131,18 +131,14 @@ def mxfp4_quantize(w: torch.Tensor, blocks=None, scales=None, stream=None):
 
 def mxfp4_dequantize(blocks: torch.Tensor, scales: torch.Tensor, out_dtype=torch.float32,
                      out=None, stream=None):
-    """(..., K/2) uint8 + (..., K/32) uint8 -> (..., K) fp32 or bf16."""
-    if stream is None and (out_dtype is torch.bfloat16 or out_dtype is torch.float32):
-        return (_ops or _host_ops()).dequantize(blocks, scales, out, out_dtype is torch.float32)
-    _dev(blocks, torch.uint8, "blocks")
-    _dev(scales, torch.uint8, "scales")
-    K = blocks.shape[-1] * 2
-    rows = blocks.numel() // blocks.shape[-1] if blocks.shape[-1] else 0
-    code = OUT_F32 if out_dtype == torch.float32 else OUT_BF16
-    if out is None:
-        out = torch.empty(*blocks.shape[:-1], K, dtype=out_dtype, device=blocks.device)
-    _call("mxfp4_dequantize", _ptr(blocks), _ptr(scales), rows, K, _ptr(out), code, _stream(stream))
-    return out
+    """(..., K/2) uint8 + (..., K/32) uint8 -> (..., K) fp32 or bf16 (out_dtype, also of a given
+    out). Runs on the tensors' device."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mxfp4_dequantize(blocks, scales, out_dtype, out)
+    if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
+        raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+    return (_ops or _host_ops()).dequantize(blocks, scales, out, out_dtype is torch.float32)
 
 
 # --------------------------------------------------------------------- routing -----

@@ -111,6 +111,16 @@ T* dense(const Tensor* t, at::ScalarType type, at::IntArrayRef shape, int dev, c
   return t ? dense<T>(*t, type, shape, dev, name) : nullptr;
 }
 
+// a dense tensor of that type and device, of any shape
+void check_dense(const Tensor& t, at::ScalarType type, int dev, const char* name) {
+  if (t.scalar_type() != type || !t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
+    refuse(t, type, nullptr, dev, name);
+}
+void check_count(const Tensor& t, int64_t count, const char* name) {
+  if (t.numel() != count)
+    throw std::invalid_argument(std::string(name) + " must have " + std::to_string(count) + " elements, got " + text(t.sizes()));
+}
+
 void check_bf16(const Tensor& t, int dev, const char* name) {
   if (t.scalar_type() != at::kBFloat16 || !t.is_cuda() || t.get_device() != dev)
     refuse(t, at::kBFloat16, nullptr, dev, name);
@@ -359,25 +369,28 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// blocks, scales, out (fp32 or bf16, as long as the rows it takes) -> out
+// blocks, scales, out, fp32 (else bf16) -> out. scales and a given out may have any shape of the right
+// number of elements. Everything is checked before the first pointer is taken.
 PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 4, [&]() -> PyObject* {
     const Tensor &blocks = tensor(a[0], "blocks"), &scales = tensor(a[1], "scales");
     const int dev = device_of(blocks, "blocks");
-    const uint8_t* b = dense<uint8_t>(blocks, at::kByte, blocks.sizes(), dev, "blocks");
-    const uint8_t* s = dense<uint8_t>(scales, at::kByte, scales.sizes(), dev, "scales");
+    check_dense(blocks, at::kByte, dev, "blocks");
+    check_dense(scales, at::kByte, dev, "scales");
     if (blocks.dim() < 1) throw std::invalid_argument("blocks must have at least one dimension");
     const int64_t half = blocks.sizes().back(), rows = half ? blocks.numel() / half : 0;
+    check_count(scales, rows * (half / 16), "scales");
     const bool f32 = a[3] == Py_True;
+    const at::ScalarType type = f32 ? at::kFloat : at::kBFloat16;
     const Tensor* given = optional(a[2], "out");
-    Tensor out;
     if (given) {
-      out = *given;
-    } else {
-      std::vector<int64_t> shape(blocks.sizes().begin(), blocks.sizes().end());
-      shape.back() = 2 * half;
-      out = fresh(shape, blocks, f32 ? at::kFloat : at::kBFloat16);
+      check_dense(*given, type, dev, "out");
+      check_count(*given, rows * 2 * half, "out");
     }
+    std::vector<int64_t> shape(blocks.sizes().begin(), blocks.sizes().end());
+    shape.back() = 2 * half;
+    const Tensor out = given ? *given : fresh(shape, blocks, type);
+    const auto *b = static_cast<const uint8_t*>(blocks.data_ptr()), *s = static_cast<const uint8_t*>(scales.data_ptr());
     on_device(dev, "mxfp4_dequantize", [&](void* st) {
       return p_dequantize(b, s, rows, 2 * half, out.data_ptr(), f32 ? MXMOE_OUT_F32 : MXMOE_OUT_BF16, st);
     });

@@ -153,3 +153,28 @@ def test_quantize_round_to_grid_exhaustive_fp32(B):
             gblk, gsc = B.mxfp4_quantize(torch.from_numpy(blocks).cuda())
             assert np.array_equal(gsc.cpu().numpy(), osc), (negative, lo)
             assert np.array_equal(gblk.cpu().numpy(), oblk), (negative, lo)
+
+
+def test_dequantize_given_output_and_stream(B):
+    """A given out is written whole and nothing beside it; a given stream takes the same checks."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.randn(5, 96, generator=g, device="cuda")
+    blocks, scales = B.mxfp4_quantize(w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for dt in (torch.float32, torch.bfloat16):
+        want = B.mxfp4_dequantize(blocks, scales, dt)
+        for kw in ({}, {"stream": s}):
+            buf = torch.full((7, 96), 7.0, dtype=dt, device="cuda")
+            torch.cuda.synchronize()
+            out = buf[1:6]
+            assert B.mxfp4_dequantize(blocks, scales, dt, out=out, **kw) is out
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and bool((buf[0] == 7).all()) and bool((buf[6] == 7).all())
+            other = torch.bfloat16 if dt is torch.float32 else torch.float32
+            for bad in (dict(out=buf[1:5]), dict(out=buf[1:6].to(other)), dict(out=buf[1:6].cpu()),
+                        dict(out=torch.empty(96, 5, dtype=dt, device="cuda").t()), dict(scales=scales[:4])):
+                args = dict(dict(blocks=blocks, scales=scales), **bad)
+                with pytest.raises(ValueError):
+                    B.mxfp4_dequantize(out_dtype=dt, **args, **kw)
+    B.mxmoe_check()

@@ -52,3 +52,36 @@ def test_the_binding_hands_over_the_library_s_own_entry_points():
     import re
     asked = re.findall(r'address\("(\w+)"\)', src)
     assert len(asked) == 6 and set(asked) <= set(binding._SIGS)
+
+
+def _fake_cuda(*shape, dtype=torch.uint8, device="cuda:0"):
+    """A tensor that says it is on a GPU and holds nothing: whatever reads its address fails."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        return torch.empty(*shape, dtype=dtype, device=device)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake CUDA tensors: CPU only")
+@pytest.mark.parametrize("change,match", [
+    (dict(scales=(4, 1)), "scales must have 8 elements"), (dict(scales=(3, 2)), "scales must have 8 elements"),
+    (dict(scales=(5, 2)), "scales must have 8 elements"), (dict(scales=(4, 2), sdt=torch.int8), "scales must be Byte"),
+    (dict(out=(4, 32)), "out must have 256 elements"), (dict(out=(3, 64)), "out must have 256 elements"),
+    (dict(out=(8, 64)), "out must have 256 elements"), (dict(odt=torch.bfloat16), "out must be Float"),
+    (dict(odt=torch.float16), "out must be Float"), (dict(f32=False), "out must be BFloat16"),
+    (dict(odev="cpu"), "out must be a CUDA tensor"), (dict(odev="cuda:1"), "out is on cuda:1"),
+    (dict(sdev="cuda:1"), "scales is on cuda:1"), (dict(strided=True), "out must be contiguous")])
+def test_dequantize_refuses_what_does_not_fit(ops, change, match):
+    c = dict(dict(scales=(4, 2), sdt=torch.uint8, sdev="cuda:0", out=(4, 64), odt=torch.float32, odev="cuda:0", f32=True,
+                  strided=False), **change)
+    out = _fake_cuda(*c["out"], dtype=c["odt"], device=c["odev"])
+    if c["strided"]:
+        out = _fake_cuda(64, 4, dtype=c["odt"]).t()
+    with pytest.raises(ValueError, match=match):
+        ops.dequantize(_fake_cuda(4, 32), _fake_cuda(*c["scales"], dtype=c["sdt"], device=c["sdev"]), out, c["f32"])
+
+
+def test_dequantize_knows_two_output_types():
+    from mxfp4_block_scaled_moe_b200 import binding
+    t = torch.zeros(4, 32, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="out_dtype"):
+        binding.mxfp4_dequantize(t, t, torch.float16)
