@@ -148,11 +148,18 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t (&r)[4]) {
                : "r"(at)
                : "memory");
 }
-// byte k of a word as the exponent field of an fp32: 2^(byte - 127). Byte 0 reads as zero: its
-// block's values are below 2^-124.
+// byte k of a word as the exponent field of an fp32: 2^(byte - 127). As a key's factor byte 0 reads as
+// zero: its block's values are below 2^-124.
 __device__ __forceinline__ uint32_t exponent_of(uint32_t word, int k) {
   return (k < 3 ? word << (23 - 8 * k) : word >> 1) & 0x7F800000u;
 }
+
+// An item's sums carry 2^(15 + 127 - E), E the largest value scale byte of the block: times 2^-15 (and
+// the row's 1 / l) they are at most a value, and times 2^(E - 127) then the outputs. In one factor
+// 2^(E - 142) would be below the normal numbers for E < 16, and lost.
+constexpr float kUndo = 0x1p-15f;
+// 2^(e - 127) of an fp32's exponent field; the least, 2^-127, is a subnormal
+__device__ __forceinline__ float power_of(int field) { return __int_as_float(max(field, 1 << 22)); }
 
 // r / G for the rows of an item: r G < 2^32, so the rounded-up reciprocal is exact
 __device__ __forceinline__ int query_of(const KvAttentionArgs& p, int r) {
@@ -753,9 +760,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
           if (g == 0) reinterpret_cast<float2*>(factors)[r] = make_float2(m[i][x] * qs[i][x], sum);
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k) {
-            const float f = ex2(static_cast<float>((E[k] >> 23) - 142));
+            const float f = power_of(E[k]);
             *reinterpret_cast<float4*>(mine + r * D + 32 * k + 4 * g) =
-                make_float4(o[i][k][0][x] * f, o[i][k][0][x + 2] * f, o[i][k][1][x] * f, o[i][k][1][x + 2] * f);
+                make_float4(o[i][k][0][x] * kUndo * f, o[i][k][0][x + 2] * kUndo * f, o[i][k][1][x] * kUndo * f,
+                            o[i][k][1][x + 2] * kUndo * f);
           }
         }
       asm volatile("bar.sync %0, %1;\n" ::"r"(1 + warp / ways), "r"(32 * ways) : "memory");
@@ -809,23 +817,24 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
           const int qi = query_of(p, row), hd = h * p.G + row - qi * p.G;
           const float base = m[i][x] == -INFINITY ? 0.f : m[i][x] * qs[i][x];
           if (p.sinks) sum += ex2(__ldg(p.sinks + hd) * 1.44269504088896f - base);
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          const float inv = sum > 0.f ? kUndo / sum : 0.f;
           uint16_t* dst = p.out + ((static_cast<int64_t>(cur.b) * p.Lq + qi) * p.Hkv * p.G + hd) * D + c0;
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k) {
-            const float f = ex2(static_cast<float>((E[k] >> 23) - 142)) * inv;
+            const float f = power_of(E[k]);
             *reinterpret_cast<uint2*>(dst + 32 * k) =
-                make_uint2(pack_bf16(o[i][k][0][x] * f, o[i][k][0][x + 2] * f),
-                           pack_bf16(o[i][k][1][x] * f, o[i][k][1][x + 2] * f));
+                make_uint2(pack_bf16(o[i][k][0][x] * inv * f, o[i][k][0][x + 2] * inv * f),
+                           pack_bf16(o[i][k][1][x] * inv * f, o[i][k][1][x + 2] * inv * f));
           }
         } else if (row < p.R) {
           if (g == 0) p.part_ml[slot * S::kRows + r] = make_float2(m[i][x] * qs[i][x], sum);
           float* dst = p.part + (slot * S::kRows + r) * D + c0;
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k) {
-            const float f = ex2(static_cast<float>((E[k] >> 23) - 142));
+            const float f = power_of(E[k]);
             *reinterpret_cast<float4*>(dst + 32 * k) =
-                make_float4(o[i][k][0][x] * f, o[i][k][0][x + 2] * f, o[i][k][1][x] * f, o[i][k][1][x + 2] * f);
+                make_float4(o[i][k][0][x] * kUndo * f, o[i][k][0][x + 2] * kUndo * f, o[i][k][1][x] * kUndo * f,
+                            o[i][k][1][x + 2] * kUndo * f);
           }
         }
       }

@@ -1,0 +1,60 @@
+"""mxfp4_kv_attention at the ends of its ranges: the least values a cache holds, keys that only some of
+a call's queries see, lengths near the largest.
+
+Bar: that of test_gpu_kv_cache.py (a bf16 rounding, 2^-8; 11-bit weights and the scores' error,
+2^-11 + 2^-13 of the sum of magnitudes; 2^-36 of the largest value that the query sees), and half of
+bf16's least step, 2^-134, with as much again for the fp32 sums' own least step.
+"""
+import pytest
+import torch
+
+from test_gpu_kv_cache import Case, _decode
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mxfp4_block_scaled_moe_b200 import binding
+    return binding
+
+
+def check(c, out, queries=None):
+    """Every query of the case (or those (sequence, query) given) against the formula in 64 bits, a
+    32-column block of a key/value head at a time for the values' size."""
+    lens, G = c.lens.tolist(), c.Hq // c.Hkv
+    for b, n in enumerate(lens):
+        used = c.table[b, :-(-n // c.page)].long()
+        k, v = (_decode(c.cache[i][used], c.cache[i + 1][used]).transpose(1, 2).flatten(0, 1)[:n] for i in (0, 2))
+        pos = torch.arange(n, device="cuda")
+        for i in range(c.Lq):
+            if queries is not None and (b, i) not in queries:
+                continue
+            p = n - c.Lq + i
+            seen = (pos <= p) & (pos > p - c.window) if c.window else pos <= p
+            kk, vv = k[seen], v[seen]
+            z = torch.einsum("hgd,nhd->hgn", c.q[b, i].double().view(c.Hkv, G, c.D), kk) * c.D ** -0.5
+            if c.sinks is not None:
+                z = torch.cat((z, c.sinks.double().view(c.Hkv, G, 1)), -1)
+            w = torch.softmax(z, -1)[..., :kk.shape[0]]
+            ref = torch.einsum("hgn,nhd->hgd", w, vv)
+            mag = torch.einsum("hgn,nhd->hgd", w, vv.abs())
+            top = vv.abs().amax(0).unflatten(-1, (-1, 32)).amax(-1).repeat_interleave(32, -1)[:, None] if kk.shape[0] else 0.0
+            err = (out.view(c.n, c.Lq, c.Hkv, G, c.D)[b, i].double() - ref).abs()
+            ok = err <= ref.abs() * 2.0 ** -8 + mag * (2.0 ** -11 + 2.0 ** -13) + top * 2.0 ** -36 + 2.0 ** -133
+            assert bool(ok.all()), (b, i, n, float(err.max()), float(ref.abs().max()))
+
+
+@pytest.mark.parametrize("less", [90, 105, 112, 118, 124, 127])
+@pytest.mark.parametrize("D,lens,Hq,window", [(64, [90, 700], 16, 0), (128, [5000, 40], 8, 0), (64, [2000], 16, 100),
+                                              (64, [300], 48, 0)])
+def test_small_values(B, D, lens, Hq, window, less):
+    """Value scale bytes down to 0, by each way an output is written (by the warp that holds its item, by
+    the joining kernel, by warps that share an item)."""
+    c = Case(B, lens, 1, Hq, 2, D, 16, window=window, sinks=True, vspread=1.0)
+    s = c.cache[3]
+    c.cache[3] = torch.where(s == 255, s.int(), (s.int() - less).clamp(min=0)).to(torch.uint8)
+    out = c.run(B)
+    B.mxmoe_check()
+    assert bool(out.any())
+    check(c, out)
