@@ -343,7 +343,10 @@ int mxfp4_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t l
  * bf16 (B, Lq, Hq, D). Cache places that no query sees may hold anything.
  * Scores, maxima, sums and outputs are fp32 until the last rounding; weights are rounded to
  * 11 bits (and to 2^-40 of a 32-column block's largest value scale) before the product with
- * the values. Sums are joined in a fixed order: the same call gives the same bits.
+ * the values. Sums are joined in a fixed order: the same call gives the same bits. What a query's
+ * mask hides has no part in its output, infinities and NaN in other queries' keys included; where
+ * queries of a call see different keys, a value more than 2^110 above the rest may overflow for
+ * those that see it.
  * workspace: device memory of mxfp4_kv_attention_workspace's size, 16-byte aligned, the call's
  * own until it has run (calls on two streams need two); it needs no initialization.
  * Limits: D 64 or 128, Hq a multiple of Hkv, Hq <= 1024, Lq <= 128, B <= 65536, page sizes as

@@ -16,7 +16,10 @@
 //  - O^T += V^T P^T: the value scales multiply the weights, p 2^(e_j - E + 15), where E is the
 //    largest value exponent seen so far in that 32-value block; the weights are then rounded
 //    to f16 (11 bits; absolute floor 2^-40 of the largest scale). Maximum, sum, and all
-//    accumulators are fp32.
+//    accumulators are fp32. The rows of a tile share E. Where they belong to queries that see
+//    different keys, only keys that all of them see set it, and one that some see and that lies
+//    above it (an infinite value behind another query's mask, first of all) is added in fp32
+//    beside the matrix products: no query's precision hangs on a key that it does not see.
 // Row maxima, sums and E stay with the warp and its accumulators are rescaled only in units
 // where one of them grows.
 //
@@ -112,6 +115,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
+  return make_float2(__half2float(__ushort_as_half(static_cast<unsigned short>(v))),
+                     __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16))));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -160,6 +168,13 @@ __device__ __forceinline__ uint32_t exponent_of(uint32_t word, int k) {
 constexpr float kUndo = 0x1p-15f;
 // 2^(e - 127) of an fp32's exponent field; the least, 2^-127, is a subnormal
 __device__ __forceinline__ float power_of(int field) { return __int_as_float(max(field, 1 << 22)); }
+
+// 2^d, which may lie outside of fp32, as two finite factors: a zero stays a zero
+struct Power2 {
+  float a, b;
+  __device__ __forceinline__ explicit Power2(int d)
+      : a(ex2(static_cast<float>(min(d >> 1, 127)))), b(ex2(static_cast<float>(min(d - (d >> 1), 127)))) {}
+};
 
 // r / G for the rows of an item: r G < 2^32, so the rounded-up reciprocal is exact
 __device__ __forceinline__ int query_of(const KvAttentionArgs& p, int r) {
@@ -244,7 +259,10 @@ __device__ __forceinline__ int open_at(const KvAttentionArgs& p, Cursor<kUnit>& 
   return start;
 }
 
-template <int D, int NT>
+// kMulti: a row tile may hold rows of several queries. Calls without such tiles take a kernel of their own,
+// because what E needs here shows in the loop's schedule: 64 sequences of two queries 54.1 us instead of
+// 52.1, 3 long ones of D = 128 83.9 instead of 79.7. (Taking such a part anew, query by query: 88.2.)
+template <int D, int NT, bool kMulti>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel(const KvAttentionArgs p) {
   using S = Shape<D, NT>;
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
@@ -500,7 +518,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
     }
     // keys that some row (seen) and that every row (full) of the tile sees
     const int hi_first = len - p.Lq + query_of(p, row0) + 1;
-    const int hi_last = len - p.Lq + query_of(p, min(row0 + S::kRows, p.R) - 1) + 1;
+    const int hi_last = kMulti ? len - p.Lq + query_of(p, min(row0 + S::kRows, p.R) - 1) + 1 : hi_first;
     const int seen_lo = p.window > 0 ? max(0, hi_first - p.window) : 0, seen_hi = max(hi_last, 0);
     const int full_lo = p.window > 0 ? max(0, hi_last - p.window) : 0, full_hi = hi_first;
 
@@ -518,6 +536,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
     }
 #pragma unroll
     for (int k = 0; k < S::kBlocks; ++k) E[k] = 0;
+    unsigned lone = 0;   // blocks whose E is of keys that some queries do not see: no other has come yet
 
     // ---- its units in this run ----
     for (; at < end; ++at) {
@@ -550,21 +569,30 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
       // The unit's scales as fp32: the keys' own, the values' as weight factors 2^(15 + e - E). A
       // lane takes keys lane (and lane + 32). A key that no row sees counts as scale 0: what
       // lies in its place does not matter.
-      const bool edge = pages != (1u << S::kTiles) - 1 || key0 < full_lo || key0 + S::kUnit > full_hi;
-      uint32_t top[S::kBlocks];
+      const bool edge = pages != (1u << S::kTiles) - 1 || key0 < full_lo || key0 + S::kUnit > full_hi || (kMulti && lone);
+      // the value scales of one of the lane's keys, 0 if no row sees it
+      const auto seen_scales = [&](int e) -> uint32_t {
+        const int key = key0 + 32 * e + lane;
+        if (key < seen_lo || key >= seen_hi || !((pages >> (2 * e + (lane >> 4))) & 1)) return 0;
+        return lds_scales<S::kBlocks>(ssv + (32 * e + lane) * S::kBlocks);
+      };
+      uint32_t top[S::kBlocks], es[S::kUnit / 32];   // es: the scales that set E, of keys that all queries see
+#pragma unroll
+      for (int e = 0; e < S::kUnit / 32; ++e) es[e] = ev[e];
       if (edge) {
 #pragma unroll
         for (int e = 0; e < S::kUnit / 32; ++e) {
           const int key = key0 + 32 * e + lane;
           if (key < seen_lo || key >= seen_hi || !((pages >> (2 * e + (lane >> 4))) & 1)) ev[e] = 0;
+          es[e] = kMulti && (key < full_lo || key >= full_hi) ? 0 : ev[e];
         }
       }
       bool higher = false;
 #pragma unroll
       for (int k = 0; k < S::kBlocks; ++k) {
-        top[k] = exponent_of(ev[0], k);
+        top[k] = exponent_of(es[0], k);
 #pragma unroll
-        for (int e = 1; e < S::kUnit / 32; ++e) top[k] = max(top[k], exponent_of(ev[e], k));
+        for (int e = 1; e < S::kUnit / 32; ++e) top[k] = max(top[k], exponent_of(es[e], k));
         higher |= static_cast<int>(top[k]) > E[k];
       }
       if (__any_sync(0xffffffffu, higher)) {
@@ -630,7 +658,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
           }
         }
       }
+      bool above = kMulti && lone;   // does a key that only some rows see lie above E?
       if (edge) {
+        if (kMulti) {
+          uint32_t bound = 0;
+#pragma unroll
+          for (int k = 0; k < S::kBlocks; ++k) bound |= static_cast<uint32_t>(E[k] >> 23) << (8 * k);
+#pragma unroll
+          for (int e = 0; e < S::kUnit / 32; ++e) above |= __vmaxu4(seen_scales(e), bound) != bound;
+        }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           int hi[2], lo[2];
@@ -703,6 +739,83 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
           }
         l[i][0] = lo_of(sum);
         l[i][1] = hi_of(sum);
+      }
+      if (kMulti && __any_sync(0xffffffffu, above)) {
+        // Blocks whose E is of such keys alone take the least of them; a key that all rows see then
+        // sets E anew, lower if need be. Keys above E leave the matrix products and are added here.
+        unsigned apart[S::kUnit / 32];
+        uint32_t out = 0, v[S::kUnit / 32];
+#pragma unroll
+        for (int e = 0; e < S::kUnit / 32; ++e) v[e] = seen_scales(e);
+#pragma unroll
+        for (int k = 0; k < S::kBlocks; ++k) {
+          uint32_t most = 0, least = 255;
+#pragma unroll
+          for (int e = 0; e < S::kUnit / 32; ++e) {
+            const int key = key0 + 32 * e + lane;
+            const uint32_t x = v[e] >> (8 * k) & 255;
+            if (key >= full_lo && key < full_hi) most = max(most, x);
+            else if (x) least = min(least, x);
+          }
+          most = __reduce_max_sync(0xffffffffu, most);
+          least = __reduce_min_sync(0xffffffffu, least);
+          const int was = E[k] >> 23;
+          int next = was;
+          if ((lone >> k) & 1) {
+            next = most ? most : min(static_cast<uint32_t>(was), least);
+            if (most) lone &= ~(1u << k);
+          } else if (was == 0 && least < 255) {
+            next = least;
+            lone |= 1u << k;
+          }
+          const Power2 f(was - next);
+          E[k] = next << 23;
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              o[i][k][0][x] = o[i][k][0][x] * f.a * f.b;
+              o[i][k][1][x] = o[i][k][1][x] * f.a * f.b;
+            }
+#pragma unroll
+          for (int e = 0; e < S::kUnit / 32; ++e)
+            if (static_cast<int>(v[e] >> (8 * k) & 255) > next) out |= 1u << e;
+        }
+#pragma unroll
+        for (int e = 0; e < S::kUnit / 32; ++e) {
+          apart[e] = __ballot_sync(0xffffffffu, (out >> e) & 1);
+#pragma unroll
+          for (int k = 0; k < S::kBlocks; ++k)
+            factors[(32 * e + lane) * 2 * S::kBlocks + S::kBlocks + k] =
+                (out >> e) & 1 ? 0.f : __int_as_float(max(static_cast<int>(exponent_of(v[e], k)) - E[k] + (142 << 23), 0));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < S::kTiles; ++y)
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            for (unsigned left = (apart[y / 2] >> (16 * (y % 2) + 8 * z)) & 255; left; left &= left - 1) {
+              const int gk = __ffs(left) - 1, key = 16 * y + 8 * z + gk;
+#pragma unroll
+              for (int k = 0; k < S::kBlocks; ++k) {
+                const uint32_t codes = *reinterpret_cast<const uint16_t*>(
+                    sk + S::kKV + key * S::kRowBytes + 16 * (k ^ (kChunks == 2 ? (gk >> 2) & 1 : (gk >> 1) & 3)) + 2 * g);
+                uint32_t c[4];   // the lane's four columns: low and high half of c[0], of c[1]
+                expand(codes * 0x10001u, c);   // both halves: nvcc 12.9 makes zeros of a lone 16-bit load's bytes here
+                const float2 v0 = unpack_f16(c[0]), v1 = unpack_f16(c[1]);
+                const Power2 f(15 + ssv[key * S::kBlocks + k] - (E[k] >> 23));
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const float w = __shfl_sync(0xffffffffu, x ? hi_of(s[i][y][z]) : lo_of(s[i][y][z]), 4 * gk + t) * f.a;
+                    o[i][k][0][x] = fmaf(w * v0.x, f.b, o[i][k][0][x]);
+                    o[i][k][0][x + 2] = fmaf(w * v0.y, f.b, o[i][k][0][x + 2]);
+                    o[i][k][1][x] = fmaf(w * v1.x, f.b, o[i][k][1][x]);
+                    o[i][k][1][x + 2] = fmaf(w * v1.y, f.b, o[i][k][1][x + 2]);
+                  }
+              }
+            }
       }
       // O^T += V^T P^T
 #pragma unroll
@@ -965,12 +1078,12 @@ Layout layout(int64_t items, int R, int D, int sms) {
   return l;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kMulti>
 cudaError_t launch(KvAttentionArgs p, int sms, cudaStream_t st, int* launches) {
   using namespace kva;
   using S = Shape<D, NT>;
   static SmemLimit limit;
-  cudaError_t e = limit.raise(kv_attention_kernel<D, NT>, S::kSmem);
+  cudaError_t e = limit.raise(kv_attention_kernel<D, NT, kMulti>, S::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = sms;
   // Items of at most four units (a short window or a short table) stay in one CTA: nothing is left
@@ -988,7 +1101,7 @@ cudaError_t launch(KvAttentionArgs p, int sms, cudaStream_t st, int* launches) {
   }
   p.unit_step = S::kUnit * std::max(p.whole, 1);
   *launches = p.whole ? 1 : 2;
-  e = launch_early(kv_attention_kernel<D, NT>, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, 0, st, p);
+  e = launch_early(kv_attention_kernel<D, NT, kMulti>, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, 0, st, p);
   if (e != cudaSuccess || p.whole) return e;
   // Few items are cut into many parts each: a CTA per row, its warps over the parts.
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * p.RT;
@@ -1013,8 +1126,10 @@ cudaError_t launch_kv_attention(KvAttentionArgs p, void* workspace, int sms, cud
   p.desc = reinterpret_cast<int4*>(base + l.desc);
   p.part_ml = reinterpret_cast<float2*>(base + l.ml);
   p.part = reinterpret_cast<float*>(base + l.part);
-  if (p.D == 64) return nt == 1 ? launch<64, 1>(p, sms, st, launches) : launch<64, 2>(p, sms, st, launches);
-  return nt == 1 ? launch<128, 1>(p, sms, st, launches) : launch<128, 2>(p, sms, st, launches);
+  const bool multi = p.Lq > 1 && p.G % (8 * nt) != 0;
+  const auto pick = [&](auto one, auto several) { return (multi ? several : one)(p, sms, st, launches); };
+  if (p.D == 64) return nt == 1 ? pick(launch<64, 1, false>, launch<64, 1, true>) : pick(launch<64, 2, false>, launch<64, 2, true>);
+  return nt == 1 ? pick(launch<128, 1, false>, launch<128, 1, true>) : pick(launch<128, 2, false>, launch<128, 2, true>);
 }
 
 }  // namespace mxmoe

@@ -58,3 +58,51 @@ def test_small_values(B, D, lens, Hq, window, less):
     B.mxmoe_check()
     assert bool(out.any())
     check(c, out)
+
+
+def _slots(c, b, pos):
+    return c.table[b].long()[pos // c.page] * c.page + pos % c.page
+
+
+HIDDEN = [dict(Lq=2, Hq=16, Hkv=2, D=64, page=64, window=0), dict(Lq=2, Hq=8, Hkv=2, D=128, page=16, window=0),
+          dict(Lq=3, Hq=8, Hkv=2, D=64, page=16, window=100), dict(Lq=4, Hq=8, Hkv=2, D=128, page=32, window=37),
+          dict(Lq=2, Hq=48, Hkv=2, D=64, page=32, window=0), dict(Lq=5, Hq=6, Hkv=2, D=128, page=16, window=600),
+          dict(Lq=17, Hq=4, Hkv=2, D=64, page=64, window=0), dict(Lq=2, Hq=8, Hkv=1, D=64, page=16, window=1)]
+
+
+@pytest.mark.parametrize("case", HIDDEN, ids=[str(i) for i in range(len(HIDDEN))])
+@pytest.mark.parametrize("what", ["inf", "nan", "3e38", "1e6"])
+@pytest.mark.parametrize("lens", [[1000, 33, 300], [4, 64, 9000, 65], [128] * 40])
+def test_a_key_that_is_hidden_from_a_query_leaves_it_alone(B, case, what, lens):
+    """The last token's key and value are no numbers, or huge, in some elements: queries before it do not see
+    it, whatever the later ones of the same call make of it. The same of the first token in the first
+    query's window, which the later ones no longer see."""
+    c = Case(B, lens, sinks=True, seed=5, **case)
+    bad = torch.full((1, c.Hkv, c.D), float(what), device="cuda").bfloat16()
+    bad[:, :, 5:].mul_(0.0 if what == "1e6" else 1.0)        # an outlier in one block only, or all of them
+    if what in ("inf", "nan"):
+        bad[:, :, 40:] = 1.0
+    for place in ("last", "first"):
+        c = Case(B, lens, sinks=True, seed=5, **case)
+        for b, n in enumerate(lens):
+            at = n - 1 if place == "last" else n - c.Lq + 1 - c.window
+            if at >= 0 and (place == "last" or c.window):
+                B.mxfp4_kv_append(bad, bad, _slots(c, b, torch.tensor([at], device="cuda")), *c.cache)
+        out = c.run(B)
+        B.mxmoe_check()
+        first, last = (0, c.Lq - 1) if place == "last" else (1, c.Lq)
+        check(c, out, {(b, i) for b in range(len(lens)) for i in range(first, last)})
+        assert torch.equal(c.run(B).view(torch.int16), out.view(torch.int16))
+
+
+def test_queries_on_both_sides_of_a_huge_value(B):
+    """Queries that see a value 2^60 above the rest beside queries that do not: both are right."""
+    for D in (64, 128):
+        c = Case(B, [500, 70, 2000], 4, 8, 2, D, 16, sinks=True, seed=2)
+        for b, n in enumerate([500, 70, 2000]):
+            v = torch.full((1, 2, D), 2.0 ** 60, device="cuda").bfloat16()
+            k = torch.zeros_like(v)
+            B.mxfp4_kv_append(k, v, _slots(c, b, torch.tensor([n - 2], device="cuda")), *c.cache)
+        out = c.run(B)
+        B.mxmoe_check()
+        check(c, out)
