@@ -338,7 +338,7 @@ int mxfp4_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t l
  * device int32 (B, max_pages), page n of sequence b holding its tokens [n page_size, (n + 1)
  * page_size); entries that no query's keys need are not read (pages before the window may be
  * gone). A needed page outside [0, num_pages) counts as unseen and sets MXMOE_EDEVICE, and so
- * does a length past max_pages * page_size (cut to it). seq_lens: device int32 (B), negative
+ * does a length past max_pages * page_size or 2^30 (cut to it). seq_lens: device int32 (B), negative
  * counts as 0; the lengths stay on the device, so a captured call follows them. out: device
  * bf16 (B, Lq, Hq, D). Cache places that no query sees may hold anything.
  * Scores, maxima, sums and outputs are fp32 until the last rounding; weights are rounded to

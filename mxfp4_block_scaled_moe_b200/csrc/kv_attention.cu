@@ -49,6 +49,9 @@ namespace kva {
 
 constexpr int kJoinThreads = 256;
 
+// Keys of a sequence: positions a unit and a warp's lanes past its end, or a window before it, stay in 32 bits.
+constexpr int64_t kMaxKeys = 1 << 30;
+
 // A unit is 64 keys of 64 values or 32 of 128, 4 KB of codes: what a step's products, scores and
 // weights leave room for in registers. (32 keys of 64 values: 16 rows 47.8 us against 45.2.)
 constexpr int unit_keys(int D) { return D == 64 ? 64 : 32; }
@@ -184,8 +187,8 @@ __device__ __forceinline__ int query_of(const KvAttentionArgs& p, int r) {
 // ------------------------------------------------------------------- work line -----
 __device__ __forceinline__ int seq_len(const KvAttentionArgs& p, int b) {
   const int n = __ldg(p.seq_lens + b);
-  const int64_t cap = static_cast<int64_t>(p.max_pages) << p.page_shift;
-  if (n > cap) {   // more keys than the table has pages for
+  const int64_t cap = min(static_cast<int64_t>(p.max_pages) << p.page_shift, kMaxKeys);
+  if (n > cap) {   // more keys than the table has pages for, or than the arithmetic on keys takes
     set_device_error(p.err, MXMOE_EDEVICE);
     return static_cast<int>(cap);
   }

@@ -106,3 +106,27 @@ def test_queries_on_both_sides_of_a_huge_value(B):
         out = c.run(B)
         B.mxmoe_check()
         check(c, out)
+
+
+@pytest.mark.parametrize("n", [(1 << 30) - 1, 1 << 30, (1 << 30) + 1, (1 << 31) - 600, (1 << 31) - 1])
+@pytest.mark.parametrize("Lq,G", [(1, 8), (2, 4)])
+def test_longest_sequences(B, n, Lq, G):
+    """Lengths up to the largest int32 over a table that holds as many (its pages repeat, a window keeps the
+    work small): 2^30 keys are taken, a longer length is cut to them and reported."""
+    page, window, keep = 256, 40, min(n, 1 << 30)
+    c = Case(B, [3 * page], Lq, G, 1, 64, page, window=window)
+    table = c.table[0, torch.arange(-(-n // page), device="cuda") % 3][None].contiguous()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = B.mxfp4_kv_attention(c.q, *c.cache, table, lens, window=window)
+    if n > 1 << 30:
+        with pytest.raises(B.MxmoeError) as ei:
+            B.mxmoe_check()
+        assert ei.value.rc == B.EDEVICE
+    B.mxmoe_check()
+    # the same keys of a short sequence: the window's pages in their order
+    last = (keep - 1) // page
+    short = torch.tensor([[table[0, last - 1], table[0, last]]], dtype=torch.int32, device="cuda")
+    want = B.mxfp4_kv_attention(c.q, *c.cache, short, torch.tensor([keep - (last - 1) * page], dtype=torch.int32, device="cuda"),
+                                window=window)
+    B.mxmoe_check()
+    assert torch.equal(out, want)
