@@ -295,7 +295,8 @@ int rmsnorm_residual(const uint16_t* x, int64_t ldx, const uint16_t* residual, i
  * fp8attn-v2", Model Details) on codes that are quantized already (rmsnorm_residual's q,
  * moe_fp8_quantize), with finer scales and the rest of the projection in its epilogue:
  *   out[t, n] = bf16( act( s_x[t] s_w[n] sum_k xq[t, k] wq[n, k] + bias[n] ) + residual[t, n] )
- * all fp32 up to the one rounding. xq: device E4M3 codes (T, K); wq: device E4M3 codes (N, K);
+ * all fp32 up to the one rounding (the sum times s_x[t], then times s_w[n]; each of these has to
+ * stay in fp32's range). xq: device E4M3 codes (T, K); wq: device E4M3 codes (N, K);
  * s_x: device fp32 (T), or NULL and s_x_all for all tokens; s_w: device fp32 (N), or NULL and
  * s_w_all for all channels; bias: device fp32 (N) or NULL; act: MXMOE_ACT_NONE, _SILU or _GELU;
  * residual: device bf16 (T, N) or NULL; out: device bf16 (T, N), which may be the residual's

@@ -1187,7 +1187,10 @@ int fp8_linear_fused(const uint8_t* xq, int T, int K, const uint8_t* wq, int N, 
   if (!mxmoe::fp8_linear_supported()) return fail(MXMOE_EUNSUPPORTED, "cuTensorMapEncodeTiled is unavailable");
   Workspace* ws = nullptr;
   if (int rc = current_device_ws(&ws)) return rc;
-  const mxmoe::LinearFusedArgs a{xq, wq, s_x, s_w, (s_x ? 1.0f : s_x_all) * (s_w ? 1.0f : s_w_all),
+  // Two numbers are one factor where fp32 holds their product in full (a zero sum times an infinite
+  // one would be NaN); otherwise the sum meets them one after the other.
+  const bool one = !s_x && !s_w && std::isnormal(s_x_all * s_w_all);
+  const mxmoe::LinearFusedArgs a{xq, wq, s_x, s_w, one ? s_x_all * s_w_all : s_x_all, one ? 1.0f : s_w_all,
                                  bias, residual, out, T, K, N, act, ws->err};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   StageTimer tm(st);

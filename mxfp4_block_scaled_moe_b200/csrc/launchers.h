@@ -310,7 +310,7 @@ struct LinearFusedArgs {
   const uint8_t* wq;            // (N, K)
   const float* sx;              // (T) or null
   const float* sw;              // (N) or null
-  float s;                      // product of the scales given as numbers
+  float sx_all, sw_all;         // taken in place of sx, of sw, where that is null
   const float* bias;            // (N) or null
   const uint16_t* residual;     // (T, N) or null
   uint16_t* out;                // (T, N)

@@ -218,7 +218,7 @@ struct Columns {
   __device__ __forceinline__ void load(const LinearFusedArgs& p, int n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = both(1.f);
+      w[i] = both(p.sw_all);
       b[i] = 0;
     }
     if (p.sw) {
@@ -404,7 +404,7 @@ fp8_linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_
       const int ab = it & 1;
       const int64_t t0 = static_cast<int64_t>(u / n_tiles) * BM + 128 * rank + 32 * q;
       const int n0 = (u % n_tiles) * bn + c_first;
-      const float sx = t0 + lane < p.T ? (p.sx ? __ldg(p.sx + t0 + lane) * p.s : p.s) : 0.f;
+      const float sx = t0 + lane < p.T ? (p.sx ? __ldg(p.sx + t0 + lane) : p.sx_all) : 0.f;
       uint4 res[4], res_ahead[4];
       Columns cols, cols_ahead;
       // the lane's first element, and how many tokens are left from it on
@@ -596,7 +596,7 @@ fp8_linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid
     if (i < passes) {
       const int64_t t = t0 + mine + row0 + i * kStep;
       res[i] = residual8(p, t * p.N + n);
-      sx[i] = p.sx ? __ldg(p.sx + t) * p.s : p.s;
+      sx[i] = p.sx ? __ldg(p.sx + t) : p.sx_all;
     }
   __syncwarp();
   cluster_wait();

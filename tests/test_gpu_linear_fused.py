@@ -174,3 +174,23 @@ def test_linear_fused_activation_range(B, T, N, act):
     assert bool(B.fp8_linear_fused(xq, wq, 1.0, 1.0, bias=big, act=act).isinf().all())
     assert bool(B.fp8_linear_fused(xq, wq, 1.0, 1.0, bias=big * 0, act=act).isnan().all())
     B.mxmoe_check()
+
+
+@pytest.mark.parametrize("T,N", [(3, 64), (70, 4096), (300, 4096)])   # either kernel
+def test_scales_whose_product_leaves_fp32(B, T, N):
+    """Scales far from 1: only the scaled sums have to lie in range, not the product of the scales."""
+    c = Case(T, 1024, N)
+    one = torch.ones_like
+    for a, b in ((1e-22, 1e-22), (1e-36, 1e-5), (3e-40, 1e-3), (1e20, 1e-25), (1e25, 1e-20)):
+        for s_x, s_w in ((a, b), (a * one(c.sx), b), (a, b * one(c.sw)), (a * one(c.sx), b * one(c.sw))):
+            out = B.fp8_linear_fused(c.xq, c.wq, s_x, s_w)
+            x, w = (t.view(torch.float8_e4m3fn).double() for t in (c.xq, c.wq))
+            s = float(torch.tensor(a, dtype=torch.float32)) * float(torch.tensor(b, dtype=torch.float32))
+            y, mag = (x @ w.t()) * s, (x.abs() @ w.abs().t()) * s
+            # the bar above, and half a least step of bf16's and fp32's subnormals; a step of sum * s_x that is subnormal
+            tol = y.abs() * 2.0 ** -8 + mag * (1024 / 32 + 8) * 2.0 ** -22 + 2.0 ** -134 + 2.0 ** -149 * max(1.0, b)
+            assert bool(((out.double() - y).abs() <= tol).all()), (a, b, type(s_x), type(s_w))
+    zero = torch.zeros_like(c.xq)
+    out = B.fp8_linear_fused(zero, c.wq, 1e30, 1e30, bias=c.bias)
+    assert torch.equal(out, c.bias.bfloat16().expand(T, N))
+    B.mxmoe_check()
