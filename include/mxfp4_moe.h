@@ -284,7 +284,7 @@ int moe_mxfp4_calibrate(const uint16_t* x, const uint16_t* router_w, const uint1
  * q_scale: device fp32 (T). residual and sum_out go together; y, q or both are asked for; q
  * comes with exactly one of act_scale and q_scale. sum_out may be the residual's or x's own
  * memory, and y may be x's, where that input is dense (ld = H); any other overlap is the
- * caller's error. Limits: H % 8 == 0 (MXMOE_EALIGN), H <= 32768 (MXMOE_EUNSUPPORTED), eps in
+ * caller's error. The products h * weight have to stay in fp32's range. Limits: H % 8 == 0 (MXMOE_EALIGN), H <= 32768 (MXMOE_EUNSUPPORTED), eps in
  * [1e-12, 1], act_scale in [1e-30, 1e30], every pointer 16-byte aligned (MXMOE_EINVAL).
  * One launch, no workspace: calls on several streams may overlap. T = 0 is a no-op. */
 int rmsnorm_residual(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, const uint16_t* weight,

@@ -67,10 +67,11 @@ __device__ __forceinline__ float2 row_reduce(float s, float m, float2* buf) {
   return make_float2(s, m);
 }
 
-// The thread's products v = h w and its share of sum(h^2) and max|v|. kScaled: h times
-// `by` and w times `wby` throughout.
+// The thread's products v = h w and its share of sum(h^2) and max|v|. kScaled: h times `by`
+// throughout, and the products times `up`, which the smaller of either factor takes: products below
+// 2^-96 times 2^96 then stay in range whatever the factors (a zero by a weight of 2^32 first of all).
 template <int kVec, bool kMax, bool kScaled>
-__device__ __forceinline__ void row_stats(const uint4 (&h)[kVec], const uint4 (&w)[kVec], float by, float wby,
+__device__ __forceinline__ void row_stats(const uint4 (&h)[kVec], const uint4 (&w)[kVec], float by, float up,
                                           float (&v)[kVec][8], float& s, float& m) {
   s = 0.f;
   m = 0.f;
@@ -83,11 +84,13 @@ __device__ __forceinline__ void row_stats(const uint4 (&h)[kVec], const uint4 (&
       if (kScaled) {
         a *= by;
         b *= by;
-        wa *= wby;
-        wb *= wby;
       }
       s = fmaf(a, a, s);
       s = fmaf(b, b, s);
+      if (kScaled) {
+        (fabsf(a) < fabsf(wa) ? a : wa) *= up;
+        (fabsf(b) < fabsf(wb) ? b : wb) *= up;
+      }
       v[j][2 * i] = a * wa;
       v[j][2 * i + 1] = b * wb;
       if (kMax) m = fmaxf(m, fmaxf(fabsf(v[j][2 * i]), fabsf(v[j][2 * i + 1])));
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kWarp ? 128 : 512) rmsnorm_kernel(NormArgs p) 
     for (int j = 0; j < kVec; ++j) w[j] = tid + j * lanes < nv ? __ldg(wp + tid + j * lanes) : zero;
   }
 
-  float v[kVec][8], s, m, wby = 1.0f, eps = p.eps;
+  float v[kVec][8], s, m, up = 1.0f, eps = p.eps;
   row_stats<kVec, kToken, false>(h, w, 1.0f, 1.0f, v, s, m);
   float2 st = row_reduce<kWarp>(s, m, buf[0]);
   // Powers of two that keep rare rows inside fp32: squares past its range (|h| above about
@@ -139,12 +142,12 @@ __global__ void __launch_bounds__(kWarp ? 128 : 512) rmsnorm_kernel(NormArgs p) 
   const bool big = !(st.x <= FLT_MAX), small = kToken && st.y < 0x1p-96f;
   if (big || small) {
     if (big) eps = 0.f;
-    if (small) wby = 0x1p96f;
-    row_stats<kVec, kToken, true>(h, w, big ? 0x1p-96f : 1.0f, wby, v, s, m);
+    if (small) up = 0x1p96f;
+    row_stats<kVec, kToken, true>(h, w, big ? 0x1p-96f : 1.0f, up, v, s, m);
     st = row_reduce<kWarp>(s, m, buf[1]);
   }
   const float r = rsqrtf(fmaf(st.x, 1.0f / static_cast<float>(p.H), eps));
-  const float f = r / wby;
+  const float f = r / up;
   float fq = f;
   if (kToken) {
     if (st.y > 0.f) fq = 448.0f / st.y;

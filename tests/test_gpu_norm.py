@@ -166,3 +166,33 @@ def test_refusals(B):
         with pytest.raises(B.MxmoeError) as ei:
             bad()
         assert ei.value.rc == rc
+
+
+@pytest.mark.parametrize("T", [3, 700])
+@pytest.mark.parametrize("power", [31, 32, 40, 100, 127, -40, -120])
+def test_token_scales_with_weights_far_from_one(B, T, power):
+    """Rows of zeros, with zeros and with the least values, next to weights from 2^-120 to 2^127, some of
+    them infinite products' halves: zeros stay zeros, and the rest keeps the norm's precision."""
+    H = 320
+    x, _, _ = _inputs(T, H, 11)
+    w = torch.full((H,), 2.0 ** power, device="cuda").bfloat16()
+    w[::3] = 1.0
+    w[1::7] = -(2.0 ** min(power, 126))
+    x[0] = 0
+    x[1] = 0
+    x[1, 0], x[1, 5] = 2.0 ** -133, -(2.0 ** -130)
+    x[2, ::2] = 0
+    q, sc, _ = B.rmsnorm_residual_fp8(x, w)
+    y, _ = B.rmsnorm_residual(x, w)
+    assert float(sc[0]) == 1.0 and not bool(q[0].bitwise_and(0x7F).any()) and not bool(y[0].any())
+    n = _norm64(x, w)
+    want = n.abs().amax(1) / 448
+    fits = (want > 2.0 ** -125) & (want < 2.0 ** 127)      # scales that fp32 holds to its full precision
+    fits[0] = False
+    # products h w in range: h is below 8
+    fits &= (x.double() * w.double()).abs().amax(1) < 2.0 ** 127.9
+    assert bool(fits[1:].any()) or power == 127
+    assert bool(((sc[fits].double() - want[fits]).abs() <= want[fits] * REL).all())
+    _check_q(q[fits], n[fits] / sc[fits].double()[:, None])
+    tiny = torch.isfinite(n[1]) & (n[1].abs() < 3e38)
+    assert bool((y[1].double() - n[1]).abs()[tiny].le(n[1].abs()[tiny] * (2.0 ** -8 + REL) + 2.0 ** -133).all())
