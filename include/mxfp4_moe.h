@@ -317,7 +317,7 @@ int fp8_linear_fused(const uint8_t* xq, int T, int K, const uint8_t* wq, int N, 
  *
  * mxfp4_kv_append -- write the keys and values of T tokens: row t of k and v (device bf16, (Hkv,
  * D) each, rows ldk / ldv elements apart: slices of a fused projection's output do) is
- * quantized as mxfp4_quantize does (same bits for the same values) and stored at slots[t]
+ * quantized as mxfp4_quantize does (the same bits, NaN stored as zeros) and stored at slots[t]
  * (device int64). A negative slot skips its token (padding). A slot at or past num_pages *
  * page_size is dropped and sets MXMOE_EDEVICE (see mxmoe_check). Distinct tokens have
  * distinct slots: a slot given twice in one call is left with an unspecified mix of the two.

@@ -2,7 +2,7 @@
 // D and written at slot slots[t] (page slot / page_size, place slot % page_size). The blocks
 // are those of mxfp4_quantize, bit for bit: scale byte max(0, exponent of amax - 2), each value
 // times 2^-e to the nearest e2m1 value, ties to the even code (the conversion instruction's
-// own rounding), magnitudes past 6 saturating, the sign bit kept.
+// own rounding), magnitudes past 6 saturating, the sign bit kept; a NaN counts as a zero of its sign.
 //
 // Cache layout: blocks (page, head, place, D/2), scales (page, head, place, D/32): a head's
 // places in a page are one contiguous run, which is what the attention kernel streams.
@@ -24,13 +24,22 @@ namespace {
 
 constexpr int kThreads = 128;
 
-__device__ __forceinline__ void quantize8(const uint4& v, uint32_t& codes, uint32_t& scale) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  // largest magnitude, as bf16 bits: their order is the values' order
+// largest magnitude of a block, as bf16 bits: their order is the values' order, and NaN's lie above
+__device__ __forceinline__ uint32_t largest(const uint32_t (&u)[4]) {
   uint32_t top = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu), __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
   top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  top = max(top >> 16, top & 0xFFFFu);
+  return max(top >> 16, top & 0xFFFFu);
+}
+
+__device__ __forceinline__ void quantize8(const uint4& v, uint32_t& codes, uint32_t& scale) {
+  uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t top = largest(u);
+  if (__any_sync(0xffffffffu, top > 0x7F80u)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] &= ~(__vcmpgtu2(u[i] & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu);
+    top = largest(u);
+  }
   scale = static_cast<uint32_t>(max(0, static_cast<int>(top >> 7) - 2));
   const float inv = __uint_as_float((254u - scale) << 23);
   uint32_t c[4];

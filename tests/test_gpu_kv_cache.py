@@ -382,3 +382,26 @@ def test_attention_refusals(B):
     assert ei.value.rc == B.EUNSUPPORTED
     e = c.q[:0]
     assert B.mxfp4_kv_attention(e, *c.cache, c.table[:0], c.lens[:0]).shape == e.shape
+
+
+@pytest.mark.parametrize("D", [64, 96])
+def test_append_nonfinite_values_match_the_codec(B, D):
+    """NaN of either sign and infinities, alone in a block, with numbers, and blocks of nothing else."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    x = torch.randn(40, 3, D, generator=g, device="cuda").bfloat16()
+    bits = x.view(torch.int16)
+    nan = torch.tensor([0x7FC0, -0x40, 0x7F81, -0x7F, 0x7FFF, -1], dtype=torch.int16, device="cuda")
+    bits[:6, 0, 5] = nan
+    bits[6:12, 1, 32:] = nan[:, None]
+    bits[12:18, :, ::3] = nan[:, None, None]
+    x[18:20, 0, 1], x[20:22, 2, 33] = math.inf, -math.inf
+    x[22, 1, 0], x[22, 1, 1] = math.inf, math.nan
+    x[23, 0, :] = 0.0
+    x[23, 0, 2] = math.nan
+    cache = _fresh(3, 3, 16, D)
+    B.mxfp4_kv_append(x, x, torch.arange(40, device="cuda"), *cache)
+    B.mxmoe_check()
+    blocks, scales = B.mxfp4_quantize(x.float().contiguous())
+    for i in (0, 2):
+        for got, want in ((cache[i], blocks), (cache[i + 1], scales)):
+            assert torch.equal(got.transpose(1, 2).flatten(0, 1)[:40], want)
