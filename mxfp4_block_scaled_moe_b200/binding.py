@@ -16,6 +16,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmxfp4moe.so")
+HOST_OPS_PATH = os.path.join(_HERE, "_host_ops.so")
 
 OK, EINVAL, EALIGN, EUNSUPPORTED, ECUDA, ETIMEOUT, ENOMEM, EDEVICE = 0, -1, -2, -3, -4, -5, -6, -7
 OUT_F32, OUT_BF16 = 0, 1
@@ -138,7 +139,28 @@ def mxfp4_dequantize(blocks: torch.Tensor, scales: torch.Tensor, out_dtype=torch
             return mxfp4_dequantize(blocks, scales, out_dtype, out)
     if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
         raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
-    return (_ops or _host_ops()).dequantize(blocks, scales, out, out_dtype is torch.float32)
+    ops = _ops or _host_ops(required=False)
+    if ops is not None:
+        return ops.dequantize(blocks, scales, out, out_dtype is torch.float32)
+    # a library built without the extension: the same checks and the same call from here
+    _dev(blocks, torch.uint8, "blocks")
+    _dev(scales, torch.uint8, "scales")
+    _dev(out, out_dtype, "out")
+    if blocks.dim() < 1:
+        raise ValueError("blocks must have at least one dimension")
+    half = blocks.shape[-1]
+    rows = blocks.numel() // half if half else 0
+    for t, count, name in ((scales, rows * (half // 16), "scales"), (out, rows * 2 * half, "out")):
+        if t is not None and t.device != blocks.device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {blocks.device}")
+        if t is not None and t.numel() != count:
+            raise ValueError(f"{name} must have {count} elements, got {tuple(t.shape)}")
+    if out is None:
+        out = torch.empty(*blocks.shape[:-1], 2 * half, dtype=out_dtype, device=blocks.device)
+    with torch.cuda.device(blocks.device):
+        _call("mxfp4_dequantize", _ptr(blocks), _ptr(scales), rows, 2 * half, _ptr(out),
+              OUT_F32 if out_dtype is torch.float32 else OUT_BF16, _stream())
+    return out
 
 
 # --------------------------------------------------------------------- routing -----
@@ -370,15 +392,17 @@ def moe_combine(y, topk_idx, topk_w, inv, out=None, stream=None):
 _ops = None
 
 
-def _host_ops():
-    """Load the extension (once) and hand it the library's entry points."""
+def _host_ops(required=True):
+    """Load the extension (once) and hand it the library's entry points. None if it is missing and
+    not `required`."""
     global _ops
     if _ops is None:
+        if not os.path.exists(HOST_OPS_PATH):
+            if not required:
+                return None
+            raise RuntimeError(f"{HOST_OPS_PATH} is missing: run mxfp4_block_scaled_moe_b200/build.py")
         L = lib()
-        path = os.path.join(_HERE, "_host_ops.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: run mxfp4_block_scaled_moe_b200/build.py")
-        spec = importlib.util.spec_from_file_location("_host_ops", path)
+        spec = importlib.util.spec_from_file_location("_host_ops", HOST_OPS_PATH)
         ops = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ops)
 

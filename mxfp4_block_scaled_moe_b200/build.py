@@ -6,11 +6,14 @@ and square roots, no flush-to-zero) and linked into one shared library with the 
 runtime linked statically. The library lands next to this file, inside the package.
 
 csrc/host_ops.cpp, the operators' native host side, becomes the Python extension
-_host_ops.so beside it (compiled by g++ against the installed torch).
+_host_ops.so beside it (compiled by g++ against the installed torch). The library does not
+need it: without torch it is left out, and where it cannot be compiled the library is
+linked before that is raised.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -71,8 +74,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     srcs = sources()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     headers.append(os.path.join(INCLUDE, "mxfp4_moe.h"))
+    host_ops = importlib.util.find_spec("torch") is not None
     if not force and not _stale(LIB, srcs + headers + [__file__]):
-        build_host_ops()
+        if host_ops:
+            build_host_ops()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -88,15 +93,16 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
-        host = ex.submit(build_host_ops, force)
+        host = ex.submit(build_host_ops, force) if host_ops else None
         objs = list(ex.map(compile_one, srcs))
-        host.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs, "-lpthread", "-ldl", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if host is not None:
+        host.result()
     return LIB
 
 

@@ -178,3 +178,17 @@ def test_dequantize_given_output_and_stream(B):
                 with pytest.raises(ValueError):
                     B.mxfp4_dequantize(out_dtype=dt, **args, **kw)
     B.mxmoe_check()
+
+
+def test_dequantize_without_the_extension(B, monkeypatch, tmp_path):
+    """A library built without the Python extension decodes the same."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    blocks, scales = B.mxfp4_quantize(torch.randn(33, 64, generator=g, device="cuda"))
+    want = [B.mxfp4_dequantize(blocks, scales, dt) for dt in (torch.float32, torch.bfloat16)]
+    monkeypatch.setattr(B, "_ops", None)
+    monkeypatch.setattr(B, "HOST_OPS_PATH", str(tmp_path / "none.so"))
+    for dt, w in zip((torch.float32, torch.bfloat16), want):
+        out = torch.empty_like(w)
+        assert torch.equal(B.mxfp4_dequantize(blocks, scales, dt), w)
+        assert B.mxfp4_dequantize(blocks, scales, dt, out=out) is out and torch.equal(out, w)
+    B.mxmoe_check()

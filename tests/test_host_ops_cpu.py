@@ -85,3 +85,64 @@ def test_dequantize_knows_two_output_types():
     t = torch.zeros(4, 32, dtype=torch.uint8)
     with pytest.raises(ValueError, match="out_dtype"):
         binding.mxfp4_dequantize(t, t, torch.float16)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake CUDA tensors: CPU only")
+@pytest.mark.parametrize("change,match", [
+    (dict(scales=(4, 1)), "scales must have 8 elements"), (dict(scales=(5, 2)), "scales must have 8 elements"),
+    (dict(sdt=torch.int8), "scales must be"), (dict(out=(4, 32)), "out must have 256 elements"),
+    (dict(out=(8, 64)), "out must have 256 elements"), (dict(odt=torch.bfloat16), "out must be"),
+    (dict(odev="cpu"), "out must be a CUDA tensor"), (dict(odev="cuda:1"), "out is on cuda:1"),
+    (dict(sdev="cuda:1"), "scales is on cuda:1"), (dict(strided=True), "out must be contiguous")])
+def test_dequantize_without_the_extension_refuses_the_same(monkeypatch, tmp_path, change, match):
+    from mxfp4_block_scaled_moe_b200 import binding
+    monkeypatch.setattr(binding, "_ops", None)
+    monkeypatch.setattr(binding, "HOST_OPS_PATH", str(tmp_path / "none.so"))
+    c = dict(dict(scales=(4, 2), sdt=torch.uint8, sdev="cuda:0", out=(4, 64), odt=torch.float32, odev="cuda:0",
+                  strided=False), **change)
+    out = _fake_cuda(*c["out"], dtype=c["odt"], device=c["odev"])
+    if c["strided"]:
+        out = _fake_cuda(64, 4, dtype=c["odt"]).t()
+    with pytest.raises(ValueError, match=match):
+        binding.mxfp4_dequantize(_fake_cuda(4, 32), _fake_cuda(*c["scales"], dtype=c["sdt"], device=c["sdev"]), out=out)
+
+
+def test_operators_without_the_extension_say_so(monkeypatch, tmp_path):
+    from mxfp4_block_scaled_moe_b200 import binding
+    monkeypatch.setattr(binding, "_ops", None)
+    monkeypatch.setattr(binding, "HOST_OPS_PATH", str(tmp_path / "none.so"))
+    t = torch.zeros(4, 64)
+    with pytest.raises(RuntimeError, match="none.so is missing"):
+        binding.rmsnorm_residual(t, t[0])
+
+
+def _small_library(build, monkeypatch, tmp_path):
+    """build.build() into tmp_path, of one small source file."""
+    src = tmp_path / "one.cu"
+    src.write_text('extern "C" int one() { return 1; }\n')
+    monkeypatch.setattr(build, "sources", lambda: [str(src)])
+    monkeypatch.setattr(build, "BUILD", str(tmp_path / "obj"))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "lib.so"))
+    return tmp_path / "lib.so"
+
+
+def test_the_library_is_linked_when_the_extension_cannot_be_compiled(monkeypatch, tmp_path):
+    from mxfp4_block_scaled_moe_b200 import build
+    lib = _small_library(build, monkeypatch, tmp_path)
+
+    def broken(force=False):
+        raise RuntimeError("no Python.h")
+    monkeypatch.setattr(build, "build_host_ops", broken)
+    with pytest.raises(RuntimeError, match="no Python.h"):
+        build.build(force=True)
+    assert lib.exists()
+
+
+def test_the_library_builds_without_torch(monkeypatch, tmp_path):
+    from mxfp4_block_scaled_moe_b200 import build
+    lib = _small_library(build, monkeypatch, tmp_path)
+    real = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda n, *a: None if n == "torch" else real(n, *a))
+    monkeypatch.setattr(build, "build_host_ops", lambda force=False: pytest.fail("built without torch"))
+    assert build.build(force=True) == str(lib) and lib.exists()
+    assert build.build() == str(lib)          # nothing to do
