@@ -14,6 +14,8 @@ import threading
 
 import torch
 
+from .build import host_ops_abi
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmxfp4moe.so")
 HOST_OPS_PATH = os.path.join(_HERE, "_host_ops.so")
@@ -405,6 +407,9 @@ def _host_ops(required=True):
         spec = importlib.util.spec_from_file_location("_host_ops", HOST_OPS_PATH)
         ops = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ops)
+        if ops.built_for != host_ops_abi():
+            raise RuntimeError(f"{HOST_OPS_PATH} was built for {ops.built_for}, not for {host_ops_abi()}: run "
+                               "mxfp4_block_scaled_moe_b200/build.py")
 
         def fail(rc, name):
             raise MxmoeError(rc, name, L.mxmoe_last_error().decode(errors="replace"))

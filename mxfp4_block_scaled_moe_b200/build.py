@@ -8,7 +8,8 @@ runtime linked statically. The library lands next to this file, inside the packa
 csrc/host_ops.cpp, the operators' native host side, becomes the Python extension
 _host_ops.so beside it (compiled by g++ against the installed torch). The library does not
 need it: without torch it is left out, and where it cannot be compiled the library is
-linked before that is raised.
+linked before that is raised. It carries the torch and Python it was compiled for and is
+compiled anew for others.
 """
 from __future__ import annotations
 
@@ -50,9 +51,22 @@ def _stale(lib, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def host_ops_abi() -> str:
+    """What host_ops.cpp is compiled for; the extension holds it as `built_for`."""
+    import torch
+    return f"torch {torch.__version__}, python {sys.version_info.major}.{sys.version_info.minor}"
+
+
+def _built_for(path, abi):
+    with open(path, "rb") as f:
+        return b"built for: " + abi.encode() + b"\0" in f.read()
+
+
 def build_host_ops(force: bool = False) -> str:
     src = os.path.join(CSRC, "host_ops.cpp")
-    if not force and not _stale(HOST_OPS, [src, os.path.join(INCLUDE, "mxfp4_moe.h"), __file__]):
+    abi = host_ops_abi()
+    if not force and not _stale(HOST_OPS, [src, os.path.join(INCLUDE, "mxfp4_moe.h"), __file__]) \
+            and _built_for(HOST_OPS, abi):
         return HOST_OPS
     import torch
     from torch.utils import cpp_extension
@@ -61,7 +75,8 @@ def build_host_ops(force: bool = False) -> str:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = f"{HOST_OPS}.{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[a for i in inc for a in ("-isystem", i)],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DMXMOE_BUILT_FOR="{abi}"',
+           *[a for i in inc for a in ("-isystem", i)],
            src, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

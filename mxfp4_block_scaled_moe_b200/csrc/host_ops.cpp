@@ -432,4 +432,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host_ops", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__host_ops(void) { return PyModule_Create(&module); }
+// torch's C++ interface holds for one version of it: binding.py compares `built_for` with the versions that run,
+// and build.py finds it in the file
+const char built_for[] = "built for: " MXMOE_BUILT_FOR;
+
+PyMODINIT_FUNC PyInit__host_ops(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", built_for + sizeof("built for: ") - 1) < 0) Py_CLEAR(m);
+  return m;
+}

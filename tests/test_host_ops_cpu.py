@@ -146,3 +146,27 @@ def test_the_library_builds_without_torch(monkeypatch, tmp_path):
     monkeypatch.setattr(build, "build_host_ops", lambda force=False: pytest.fail("built without torch"))
     assert build.build(force=True) == str(lib) and lib.exists()
     assert build.build() == str(lib)          # nothing to do
+
+
+def test_the_extension_is_of_this_torch(ops, monkeypatch, tmp_path):
+    """It says what it was compiled for; build_host_ops() compiles it anew for another torch, and the
+    binding refuses one of another."""
+    from mxfp4_block_scaled_moe_b200 import binding, build
+    assert ops.built_for == build.host_ops_abi() and torch.__version__ in ops.built_for
+    assert build._built_for(build.HOST_OPS, ops.built_for) and not build._built_for(build.HOST_OPS, "torch 9.9")
+    runs = []
+
+    def compiler(cmd, **kw):
+        runs.append(cmd)
+        raise RuntimeError("compiling")
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    assert build.build_host_ops() == build.HOST_OPS and not runs
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    with pytest.raises(RuntimeError, match="compiling"):
+        build.build_host_ops()
+    assert len(runs) == 1
+    monkeypatch.setattr(binding, "_ops", None)
+    monkeypatch.setattr(binding, "lib", lambda: None)
+    with pytest.raises(RuntimeError, match="was built for torch"):
+        binding._host_ops()
+    assert binding._ops is None
