@@ -105,6 +105,13 @@ def _stream(stream=None):
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _on(stream, t):
+    """The context in which `stream` is the current one; it has to be of the tensors' device."""
+    if isinstance(t, torch.Tensor) and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
 def _dev(t, dtype, name):
     if t is None:
         return None
@@ -137,7 +144,7 @@ def mxfp4_dequantize(blocks: torch.Tensor, scales: torch.Tensor, out_dtype=torch
     """(..., K/2) uint8 + (..., K/32) uint8 -> (..., K) fp32 or bf16 (out_dtype, also of a given
     out). Runs on the tensors' device."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, blocks):
             return mxfp4_dequantize(blocks, scales, out_dtype, out)
     if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
         raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
@@ -424,7 +431,7 @@ def rmsnorm_residual(x, weight, residual=None, eps=1e-5, sum_out=None, y=None, s
     weight / sqrt(mean(h^2) + eps)) over the last axis. sum_out may be `residual` (the
     stream updated in place). Strided rows of a 2-D x or residual are taken as they are."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return rmsnorm_residual(x, weight, residual, eps, sum_out, y)
     y, _, _, sum_out = (_ops or _host_ops()).norm(x, weight, residual, eps, None, sum_out, None, y, False)
     return y, sum_out
@@ -436,7 +443,7 @@ def rmsnorm_residual_fp8(x, weight, residual=None, eps=1e-5, act_scale=None, sum
     static act_scale (scale is then None), or by one scale per token, max|n| / 448 (scale:
     fp32 of x's leading shape). y, if given, receives the bf16 norm too."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return rmsnorm_residual_fp8(x, weight, residual, eps, act_scale, sum_out, q, y)
     return (_ops or _host_ops()).norm(x, weight, residual, eps, act_scale, sum_out, q, y, True)[1:]
 
@@ -450,7 +457,7 @@ def fp8_linear_fused(xq, wq, s_x, s_w, bias=None, act=None, residual=None, out=N
     one per output channel; act: None, "silu" or "gelu" (by erf); bias fp32 (N); residual
     bf16 (T, N). out may be `residual` (the stream updated in place)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, xq):
             return fp8_linear_fused(xq, wq, s_x, s_w, bias, act, residual, out)
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}, got {act!r}")
@@ -463,7 +470,7 @@ def mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales, stream=
     D/32), uint8. slots: int64 (T), page * page_size + offset; negative skips the token. k and
     v may be slices of a fused projection's rows."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, k):
             return mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales)
     (_ops or _host_ops()).append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales)
 
@@ -485,7 +492,7 @@ def mxfp4_kv_attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, s
     q's tokens may be slices of a fused projection's rows. workspace: uint8 of at least
     mxfp4_kv_attention_workspace's size, made by the call unless given."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return mxfp4_kv_attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, seq_lens, scale, window,
                                       sinks, out, workspace)
     return (_ops or _host_ops()).attention(q, k_blocks, k_scales, v_blocks, v_scales, block_table, seq_lens, scale, window,

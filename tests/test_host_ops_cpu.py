@@ -170,3 +170,18 @@ def test_the_extension_is_of_this_torch(ops, monkeypatch, tmp_path):
     with pytest.raises(RuntimeError, match="was built for torch"):
         binding._host_ops()
     assert binding._ops is None
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake CUDA tensors: CPU only")
+def test_a_stream_of_another_device_is_refused():
+    """The operators run on their tensors' device; a stream of another one would not order them."""
+    import types
+    from mxfp4_block_scaled_moe_b200 import binding as B
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    t = _fake_cuda(4, 64)
+    for call in (lambda: B.mxfp4_dequantize(t, t, stream=other), lambda: B.rmsnorm_residual(t, t, stream=other),
+                 lambda: B.rmsnorm_residual_fp8(t, t, stream=other), lambda: B.fp8_linear_fused(t, t, 1.0, 1.0, stream=other),
+                 lambda: B.mxfp4_kv_append(t, t, t, t, t, t, t, stream=other),
+                 lambda: B.mxfp4_kv_attention(t, t, t, t, t, t, t, stream=other)):
+        with pytest.raises(ValueError, match="the stream is on cuda:1, the tensors on cuda:0"):
+            call()
