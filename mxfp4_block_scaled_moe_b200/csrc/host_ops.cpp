@@ -142,7 +142,7 @@ int64_t token_stride(const Tensor& t, int dev, const char* name) {
   const auto size = t.sizes(), stride = t.strides();
   const int64_t nd = t.dim(), row = size[nd - 2] * size[nd - 1];
   if (t.is_contiguous()) return row;
-  if (stride[nd - 1] != 1 || stride[nd - 2] != size[nd - 1])
+  if (stride[nd - 1] != 1 || (size[nd - 2] != 1 && stride[nd - 2] != size[nd - 1]))
     throw std::invalid_argument(std::string(name) + ": each token's heads must be dense");
   int64_t step = -1, n = 1;
   for (int64_t d = nd - 3; d >= 0; --d) {

@@ -405,3 +405,19 @@ def test_append_nonfinite_values_match_the_codec(B, D):
     for i in (0, 2):
         for got, want in ((cache[i], blocks), (cache[i + 1], scales)):
             assert torch.equal(got.transpose(1, 2).flatten(0, 1)[:40], want)
+
+
+def test_one_head_cut_from_wider_rows(B):
+    """A single key/value head (or query head): the stride of an axis of one element has no meaning."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.randn(2, 20, 320, generator=g, device="cuda").bfloat16()
+    k, v, q = (rows[0, :, a:a + 64].unsqueeze(0).transpose(0, 1) for a in (0, 64, 128))       # (20, 1, 64)
+    assert k.stride(1) != 64 and not k.is_contiguous()
+    cache, want = _fresh(2, 1, 16, 64), _fresh(2, 1, 16, 64)
+    slots = torch.arange(20, device="cuda")
+    B.mxfp4_kv_append(k, v, slots, *cache)
+    B.mxfp4_kv_append(k.contiguous(), v.contiguous(), slots, *want)
+    assert all(torch.equal(a, b) for a, b in zip(cache, want))
+    table, lens = torch.tensor([[0, 1]] * 20, dtype=torch.int32, device="cuda"), 1 + slots.int()
+    assert torch.equal(B.mxfp4_kv_attention(q, *cache, table, lens), B.mxfp4_kv_attention(q.contiguous(), *cache, table, lens))
+    B.mxmoe_check()
