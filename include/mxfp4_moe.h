@@ -308,6 +308,12 @@ int fp8_linear_fused(const uint8_t* xq, int T, int K, const uint8_t* wq, int N, 
                      const float* s_w, float s_w_all, const float* bias, int act, const uint16_t* residual,
                      uint16_t* out, void* stream);
 
+/* fp8_linear_fused_columns -- which kernel a call of these sizes takes on the current device: the
+ * columns of its tiles of 256 tokens (64 to 256, one CTA pair each), or 0 where K is split over
+ * clusters instead. For tests and profiles: results do not depend on it beyond rounding. Errors:
+ * MXMOE_EINVAL (sizes; columns NULL), MXMOE_ECUDA. */
+int fp8_linear_fused_columns(int T, int K, int N, int* columns);
+
 /* The paged MXFP4 key/value cache of mxfp4_kv_append and mxfp4_kv_attention ("quantization_
  * mxfp4" (KerasFormers), Primitives, along the head dimension D): k_blocks, v_blocks: device
  * uint8 (num_pages, Hkv, page_size, D/2); k_scales, v_scales: device uint8 (num_pages, Hkv,

@@ -46,6 +46,7 @@ _SIGS = {
     "moe_combine": [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp],
     "rmsnorm_residual": [_vp, _i64, _vp, _i64, _vp, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "fp8_linear_fused": [_vp, _i32, _i32, _vp, _i32, _vp, _f32, _vp, _f32, _vp, _i32, _vp, _vp, _vp],
+    "fp8_linear_fused_columns": [_i32, _i32, _i32, _vp],
     "mxfp4_kv_append": [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _vp],
     "mxfp4_kv_attention_workspace": [_i32, _i32, _i32, _i32, _i32, _vp],
     "mxfp4_kv_attention": [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _i32, _vp, _vp] + [_i32] * 5
@@ -462,6 +463,14 @@ def fp8_linear_fused(xq, wq, s_x, s_w, bias=None, act=None, residual=None, out=N
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}, got {act!r}")
     return (_ops or _host_ops()).linear(xq, wq, s_x, s_w, bias, ACTS[act], residual, out)
+
+
+def fp8_linear_fused_columns(T, K, N, device=None) -> int:
+    """The tiles' columns of an fp8_linear_fused of these sizes, or 0 where it splits K instead."""
+    n = ctypes.c_int(0)
+    with torch.cuda.device(device):
+        _call("fp8_linear_fused_columns", T, K, N, ctypes.byref(n))
+    return n.value
 
 
 def mxfp4_kv_append(k, v, slots, k_blocks, k_scales, v_blocks, v_scales, stream=None):

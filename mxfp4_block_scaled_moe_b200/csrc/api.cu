@@ -1201,6 +1201,20 @@ int fp8_linear_fused(const uint8_t* xq, int T, int K, const uint8_t* wq, int N, 
   return MXMOE_OK;
 }
 
+int fp8_linear_fused_columns(int T, int K, int N, int* columns) {
+  t_last_error.clear();
+  if (T <= 0 || K <= 0 || N <= 0 || !columns)
+    return fail(MXMOE_EINVAL, "T = %d, K = %d and N = %d must be positive, columns not NULL", T, K, N);
+  Workspace* ws = nullptr;
+  if (int rc = current_device_ws(&ws)) return rc;
+  mxmoe::LinearFusedArgs a{};
+  a.T = T;
+  a.K = K;
+  a.N = N;
+  *columns = mxmoe::fp8_linear_fused_columns(a, ws->sms);
+  return MXMOE_OK;
+}
+
 // log2 of a cache's page size, or -1 if it is none of 16, 32, 64, 128, 256
 static int page_shift_of(int page_size) {
   for (int s = 4; s <= 8; ++s)

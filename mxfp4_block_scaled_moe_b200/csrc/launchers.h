@@ -318,6 +318,8 @@ struct LinearFusedArgs {
   int* err;
 };
 cudaError_t launch_fp8_linear_fused(const LinearFusedArgs& a, int sms, cudaStream_t st);
+// columns of a tile of the CTA-pair kernel where a call of these T, K and N takes it, else 0
+int fp8_linear_fused_columns(const LinearFusedArgs& a, int sms);
 
 // mxmoe_tc_rate_probe: back-to-back kind::mxf8f6f4 MMAs (M = 128, N = n) on `ctas` CTAs
 cudaError_t launch_tc_rate(int n, int with_copy, int random, int iters, int ctas, int* err, cudaStream_t st);

@@ -786,12 +786,19 @@ int64_t split_ns(const LinearFusedArgs& p, int sms) {
   return cdiv(tiles * ks, sms) * (6000 + 370 * cdiv(p.K, BK) / ks);
 }
 
+}  // namespace
+
+int fp8_linear_fused_columns(const LinearFusedArgs& p, int sms) {
+  if (p.T <= 64) return 0;
+  const int bn = pair_width(p, sms);
+  return pair_ns(p, bn, sms) < split_ns(p, sms) ? bn : 0;
+}
+
+namespace {
+
 template <int kAct>
 cudaError_t launch_act(const LinearFusedArgs& p, int sms, cudaStream_t st) {
-  if (p.T > 64) {
-    const int bn = pair_width(p, sms);
-    if (pair_ns(p, bn, sms) < split_ns(p, sms)) return launch_pair<kAct>(p, bn, sms, st);
-  }
+  if (const int bn = fp8_linear_fused_columns(p, sms)) return launch_pair<kAct>(p, bn, sms, st);
   if (p.T <= 16) return launch_split<16, kAct>(p, sms, st);
   if (p.T <= 32) return launch_split<32, kAct>(p, sms, st);
   if (p.T <= 64) return launch_split<64, kAct>(p, sms, st);

@@ -114,3 +114,10 @@ def test_linear_fused_argument_checks(L):
         assert _linear(L, **{n: None}) == EINVAL
     for n in ("xq", "wq", "out", "sx", "sw", "bias", "res"):
         assert _linear(L, **{n: MIS}) == EINVAL and "aligned" in err(L)
+
+
+def test_linear_fused_columns_argument_checks(L):
+    n = ctypes.c_int(7)
+    for T, K, N in ((0, 64, 64), (64, 0, 64), (64, 64, 0), (-1, 64, 64)):
+        assert L.fp8_linear_fused_columns(T, K, N, ctypes.byref(n)) == EINVAL and n.value == 7
+    assert L.fp8_linear_fused_columns(64, 64, 64, None) == EINVAL

@@ -194,3 +194,29 @@ def test_scales_whose_product_leaves_fp32(B, T, N):
     out = B.fp8_linear_fused(zero, c.wq, 1e30, 1e30, bias=c.bias)
     assert torch.equal(out, c.bias.bfloat16().expand(T, N))
     B.mxmoe_check()
+
+
+# sizes that take tiles of each width, in one round of them and in several, and split products
+EACH = [(140, 1600, 3608), (5465, 2304, 152), (1165, 1184, 1096), (550, 128, 4624), (250, 480, 8104), (4774, 320, 776),
+        (4204, 1664, 624), (1024, 2880, 5120), (4427, 288, 1128), (5000, 352, 488), (1784, 448, 8056), (297, 1632, 7152),
+        (4096, 352, 5120), (777, 1024, 4096), (3000, 352, 4104), (2154, 2880, 8176), (300, 8192, 1024), (128, 1024, 8192)]
+
+
+def test_each_width_is_tested(B):
+    widths = [B.fp8_linear_fused_columns(*s) for s in EACH]
+    assert set(widths) == {0, 64, 96, 128, 160, 192, 224, 256}, widths
+    assert B.fp8_linear_fused_columns(64, 1024, 4096) == 0
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    several = {w for w, (T, K, N) in zip(widths, EACH) if w and -(-T // 256) * -(-N // w) > pairs}
+    one = {w for w, (T, K, N) in zip(widths, EACH) if w and -(-T // 256) * -(-N // w) <= pairs}
+    assert several >= {96, 128, 160, 192, 224, 256} and one >= {64, 96, 128, 160, 192, 224, 256}, widths
+
+
+@pytest.mark.parametrize("T,K,N", EACH)
+def test_linear_fused_each_width(B, T, K, N):
+    c = Case(T, K, N)
+    for k in (dict(s_x=c.sx, s_w=c.sw, bias=c.bias, residual=c.res), dict(s_x=c.sx, s_w=float(c.sw[0]), act="silu")):
+        out = B.fp8_linear_fused(c.xq, c.wq, **k)
+        B.mxmoe_check()
+        c.check(out, **k)
+        assert torch.equal(B.fp8_linear_fused(c.xq, c.wq, **k), out)
