@@ -421,3 +421,51 @@ def test_one_head_cut_from_wider_rows(B):
     table, lens = torch.tensor([[0, 1]] * 20, dtype=torch.int32, device="cuda"), 1 + slots.int()
     assert torch.equal(B.mxfp4_kv_attention(q, *cache, table, lens), B.mxfp4_kv_attention(q.contiguous(), *cache, table, lens))
     B.mxmoe_check()
+
+
+@pytest.mark.parametrize("n", [31, 129, 256, 257, 385, 600])
+@pytest.mark.parametrize("Hq,Hkv,Lq", [(20, 2, 1), (6, 2, 3)])
+def test_attention_many_sequences_in_eight_warps(B, n, Hq, Hkv, Lq):
+    """As above for 9 to 16 rows of 128 columns, whose CTAs have 256 threads: their search over the sequences
+    takes one chunk of them, or several."""
+    lens = [0 if i % 7 == 3 or 40 <= i < 75 else 1 + (i * i * 37) % (700 if i % 5 else 40) for i in range(n)]
+    c = Case(B, lens, Lq, Hq, Hkv, 128, 16, sinks=True)
+    out = c.run(B)
+    B.mxmoe_check()
+    c.check(out)
+    assert torch.equal(c.run(B), out)
+
+
+@pytest.mark.parametrize("case", [dict(lens=[150, 40], Lq=128, Hq=8, Hkv=2, D=64, page=32),
+                                  dict(lens=[260], Lq=128, Hq=1, Hkv=1, D=128, page=16, window=50, sinks=True),
+                                  dict(lens=[70], Lq=3, Hq=1024, Hkv=1, D=64, page=16),
+                                  dict(lens=[70, 33], Lq=1, Hq=1024, Hkv=1024, D=64, page=16, sinks=True)])
+def test_attention_most_queries_and_heads(B, case):
+    c = Case(B, **case)
+    out = c.run(B)
+    B.mxmoe_check()
+    c.check(out)
+
+
+@pytest.mark.parametrize("width", [1, 40])
+def test_attention_most_sequences(B, width):
+    """65,536 sequences of up to 16 keys, over a table of one page each (items stay in a CTA) and a wide one
+    (a line of units); every one against the same keys read from another place of the batch."""
+    n, page = 65536, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    cache = _fresh(64, 1, page, 64)
+    k, v = (torch.randn(64 * page, 1, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    B.mxfp4_kv_append(k, v, torch.arange(64 * page, device="cuda"), *cache)
+    seq = torch.arange(n, device="cuda")
+    table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    table[:, 0] = seq % 64
+    lens = ((seq // 64) % 17).int()
+    q = torch.randn(64, 17, 2, 64, generator=g, device="cuda").bfloat16()[seq % 64, (seq // 64) % 17]
+    out = B.mxfp4_kv_attention(q, *cache, table, lens)
+    B.mxmoe_check()
+    some = 64 * 17
+    want = B.mxfp4_kv_attention(q[:some], *cache, table[:some, :1].contiguous(), lens[:some])
+    assert torch.equal(out[:some // 64 * 64], want) or float((out[:some] - want).abs().max()) < 2.0 ** -6
+    for i in range(0, n, some):
+        assert torch.equal(out[i:i + some].view(torch.int16), out[:min(some, n - i)].view(torch.int16))
+    assert not bool(out[lens == 0].any())
