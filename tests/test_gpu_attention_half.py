@@ -167,3 +167,56 @@ def test_the_norm_feeds_the_expert_layer(B):
     # the codes are those of the norm itself: one E4M3 step of the cast of its bf16 rounding at most
     a, b = q.view(torch.float8_e4m3fn).float(), B.moe_fp8_quantize(y, 0.02).view(torch.float8_e4m3fn).float()
     assert bool(((a - b).abs() <= 2.0 ** -3 * b.abs() + 2.0 ** -9).all())
+
+
+@pytest.mark.parametrize("T,E,H,I", [(1, 8, 320, 192), (8, 4, 256, 256), (16, 4, 256, 256), (40, 8, 320, 192), (77, 8, 320, 192),
+                                     (77, 8, 352, 224)])
+def test_the_norm_and_the_expert_layer_against_the_oracle(B, T, E, H, I):
+    """Norm -> expert layer -> norm with the layer's output added to the stream, eager and replayed with new
+    inputs: the norm lets its successor start early, and each path of the layer reads what it wrote. The
+    layer's output is checked against the oracle on the norm's output."""
+    import numpy as np
+    import test_gpu_layer as TL
+    from mxfp4_block_scaled_moe_b200 import inputs
+    p = TL.pack(inputs.small_layer(E=E, k=2, T=T, H=H, I=I, seed=3, router_bias=True))
+    d = TL.to_device(p)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w1, w2 = ((1 + 0.1 * torch.randn(H, generator=g, device="cuda")).bfloat16() for _ in range(2))
+    x, res = (torch.empty(T, H, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    y, out, s1 = (torch.empty_like(x) for _ in range(3))
+
+    def layer():
+        B.rmsnorm_residual(x, w1, res, sum_out=s1, y=y)
+        B.moe_mxfp4_forward(y, d["router_w"], d["router_b"], d["gu_blocks"], d["gu_scales"], d["gu_bias"], d["d_blocks"],
+                            d["d_scales"], d["d_bias"], p.lay.k, out=out)
+        return B.rmsnorm_residual(out, w2, s1)
+
+    def fill(n):
+        x.copy_(torch.randn(T, H, generator=g, device="cuda"))
+        res.copy_(n * torch.randn(T, H, generator=g, device="cuda"))
+        for t in (y, out, s1):
+            t.fill_(float("nan"))
+
+    def check(got):
+        B.mxmoe_check()
+        h = (x.float() + res.float()).bfloat16()
+        assert torch.equal(s1, h)
+        n = _norm(h.double(), w1)
+        assert bool(((y.double() - n).abs() <= n.abs() * (2.0 ** -8 + 2.0 ** -14) + 2.0 ** -133).all())
+        p.x = inputs.bits(y)
+        d["x"] = y
+        TL.check_rows(B, p, d, np.arange(T), out=out)
+        h2 = (out.float() + s1.float()).bfloat16()
+        n2 = _norm(h2.double(), w2)
+        assert torch.equal(got[1], h2)
+        assert bool(((got[0].double() - n2).abs() <= n2.abs() * (2.0 ** -8 + 2.0 ** -14) + 2.0 ** -133).all())
+
+    fill(1)
+    check(layer())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer()
+    for n in (2, 0.5):
+        fill(n)
+        graph.replay()
+        check(got)
