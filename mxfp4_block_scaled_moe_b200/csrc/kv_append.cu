@@ -25,21 +25,20 @@ namespace {
 constexpr int kThreads = 128;
 
 // largest magnitude of a block, as bf16 bits: their order is the values' order, and NaN's lie above
-__device__ __forceinline__ uint32_t largest(const uint32_t (&u)[4]) {
-  uint32_t top = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu), __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+__device__ __forceinline__ uint32_t largest(const uint4& u) {
+  uint32_t top = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
   top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
   return max(top >> 16, top & 0xFFFFu);
 }
 
-__device__ __forceinline__ void quantize8(const uint4& v, uint32_t& codes, uint32_t& scale) {
-  uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  uint32_t top = largest(u);
-  if (__any_sync(0xffffffffu, top > 0x7F80u)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] &= ~(__vcmpgtu2(u[i] & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu);
-    top = largest(u);
-  }
+__device__ __forceinline__ uint32_t without_nan(uint32_t u) {
+  return u & ~(__vcmpgtu2(u & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu);
+}
+
+// eight values of a block whose largest magnitude is `top`
+__device__ __forceinline__ void quantize8(const uint4& v, uint32_t top, uint32_t& codes, uint32_t& scale) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
   scale = static_cast<uint32_t>(max(0, static_cast<int>(top >> 7) - 2));
   const float inv = __uint_as_float((254u - scale) << 23);
   uint32_t c[4];
@@ -81,11 +80,27 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(KvAppendArgs p, int
         v[j] = __ldcs(reinterpret_cast<const uint4*>(p.v + t * p.ldv + at));
       }
     }
+    uint32_t k_top[kAtOnce], v_top[kAtOnce], most = 0;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      k_top[j] = largest(k[j]);
+      v_top[j] = largest(v[j]);
+      most = max(most, max(k_top[j], v_top[j]));
+    }
+    if (__any_sync(0xffffffffu, most > 0x7F80u)) {
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        k[j] = make_uint4(without_nan(k[j].x), without_nan(k[j].y), without_nan(k[j].z), without_nan(k[j].w));
+        v[j] = make_uint4(without_nan(v[j].x), without_nan(v[j].y), without_nan(v[j].z), without_nan(v[j].w));
+        k_top[j] = largest(k[j]);
+        v_top[j] = largest(v[j]);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       uint32_t kc, ks, vc, vs;
-      quantize8(k[j], kc, ks);
-      quantize8(v[j], vc, vs);
+      quantize8(k[j], k_top[j], kc, ks);
+      quantize8(v[j], v_top[j], vc, vs);
       if (slot[j] < 0) continue;            // a padded row, or no row at all
       if (slot[j] >= p.num_slots) {
         set_device_error(p.err, MXMOE_EDEVICE);
