@@ -122,8 +122,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(KvAppendArgs p, int
 }  // namespace
 
 // Tokens per CTA: as many as give each of its threads its two pieces, fewer where that would leave
-// SMs idle. 16384 tokens of 8 heads of 64 (42.5 MB), slices of a fused projection: 9.7 us, 4.4 TB/s;
-// 1024 tokens 2.9. With 256 threads a CTA 10.4 and 3.5, 512 11.1 and 4.8, 64 11.0 and 2.9; one piece a
+// SMs idle. 16384 tokens of 8 heads of 64 (42.5 MB), slices of a fused projection: 9.9 us, 4.3 TB/s;
+// 1024 tokens 2.8. Launch, first loads and tail are that 2.8 of it; in the rest (5.6 TB/s) the SMs issue in
+// 0.66 of the cycles. With 256 threads a CTA 10.4 and 3.5, 512 11.1 and 4.8, 64 11.0 and 2.9; one piece a
 // thread 10.9 and 2.2, four 10.4 and 3.6.
 cudaError_t launch_kv_append(const KvAppendArgs& p, int sms, cudaStream_t st) {
   const int vecs = p.Hkv * (p.D / 8);

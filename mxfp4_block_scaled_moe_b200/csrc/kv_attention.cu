@@ -31,11 +31,13 @@
 // joined in run order by a second small kernel. Items of a few units (a short window) stay in
 // one CTA. Nothing in the result depends on timing, and no counter outlives a call.
 //
-// Measured on a B200 (time, of the bytes that must be read): 64 sequences of 500 to 8192 keys, 64
-// heads over 8 of 64 (154 MB): 44.9 us, 3.4 TB/s; 3 sequences of up to 131072 keys, 2 queries each,
-// 32 heads over 8 of 128 (318 MB): 78.6 us, 4.0 TB/s; one query over a window of 128: 4.8 us. Of
-// the first, about 9 us are launches, the start's chain of loads (lengths, table, keys) and the
-// joining kernel. The products are paced by the integer pipe (code expansion, 64 lanes a cycle:
+// Measured on a B200 (calls in a row, of the bytes that must be read): 64 sequences of 500 to 8192
+// keys, 64 heads over 8 of 64 (154 MB): 46 us, 3.3 TB/s; 3 sequences of up to 131072 keys, 2 queries
+// each, 32 heads over 8 of 128 (318 MB): 84 us (up to 91 in long loops, where the power cap lowers the
+// clock), 3.8 TB/s; one query over a window of 128: 5.8 us (4.8 in a graph). Of the first, about 9 us
+// are launches, the start's chain of loads (lengths, table, keys) and the joining kernel. Many
+// queries a sequence read and expand every key again for each 16 rows: 128 queries of 64 heads over 8
+// of 64 take 111 us over 8192 keys and 361 over 32768 (154 and 190 TF/s). The products are paced by the integer pipe (code expansion, 64 lanes a cycle:
 // half of the cycles), the matrix instructions, which on this part take issue slots from it (an
 // m16n8k16 between such instructions costs about 5 cycles beyond its own 8), and by latency: twelve
 // warps issue in half of the cycles, and more do not fit the registers.
@@ -263,7 +265,7 @@ __device__ __forceinline__ int open_at(const KvAttentionArgs& p, Cursor<kUnit>& 
 }
 
 // kMulti: a row tile may hold rows of several queries. Calls without such tiles take a kernel of their own,
-// because what E needs here shows in the loop's schedule: 64 sequences of two queries 54.1 us instead of
+// because what E needs here shows in the loop's schedule: 32 sequences of two queries 54.1 us instead of
 // 52.1, 3 long ones of D = 128 83.9 instead of 79.7. (Taking such a part anew, query by query: 88.2.)
 template <int D, int NT, bool kMulti>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel(const KvAttentionArgs p) {

@@ -120,7 +120,9 @@ __device__ __forceinline__ void send_bulk(uint32_t dst, const void* src, uint32_
                "r"(smem_u32(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
-// relaxed: it tells of tensor memory that has been read (and waited for), and is not to wait for the outputs
+// Relaxed, since a release would wait for the outputs. What it tells is that this warp has read the accumulator:
+// those reads have ended (tcgen05.wait::ld), and the fence before it orders them ahead. No memory
+// is handed over, and that is all that the next products' writes to the accumulator rest on.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
 }
@@ -756,9 +758,10 @@ cudaError_t launch_split(const LinearFusedArgs& p, int sms, cudaStream_t st) {
 //
 // A pair's chunk of K is bound by what one SM draws from L2 (its 128 rows and half of the weights'),
 // and more of it the more SMs draw at once; a narrow tile costs more loads for each product but
-// fills the last round better. E.g. 4096 x 2880 -> 5120: 256 columns 57.8 us, 224 55.4, 160 62.8;
-// 1024 x 2880 -> 5120: 160 22.2, 256 26.3, 64 36.9; 200 x 2880 -> 5120: 96 11.1, 256 14.5; 1000 x 8192 ->
-// 256: 64 17.9, 160 19.9, 256 25.7; 777 x 1024 -> 4096: 256 11.1, 128 11.8, 64 13.9.
+// fills the last round better. E.g. 4096 x 2880 -> 5120: 256 columns 52.2 us, 224 50.9, 160 59.5;
+// 1024 x 2880 -> 5120: 160 19.8, 256 23.3, 64 33.7; 200 x 2880 -> 5120: 96 10.3, 256 13.7; 1000 x 8192 ->
+// 256: 64 17.8, 160 19.2, 256 24.6; 777 x 1024 -> 4096: 256 9.6, 128 9.4, 64 11.6. (The model was fitted
+// to the kernel before its last epilogue, 5 to 10 % slower throughout.)
 int64_t pair_ns(const LinearFusedArgs& p, int bn, int sms) {
   using namespace linf;
   const int64_t nk = cdiv(p.K, BK), pairs = std::max(1, sms / 2);
@@ -775,10 +778,10 @@ int pair_width(const LinearFusedArgs& p, int sms) {
   return best;
 }
 
-// The split kernel's, 128 tokens wide. E.g. (pairs, split) 128 x 512 -> 640: 5.6 us, 6.3; 128 x 1024 ->
-// 8192: 8.4, 7.6; 128 x 8192 -> 1024: 17.9, 9.7; 200 x 2880 -> 5120: 11.1, 15.2; 300 x 8192 -> 1024: 18.3,
-// 11.3; 300 x 4096 -> 4096: 13.9, 18.4; 4000 x 8192 -> 256: 22.0, 17.9. Up to 64 tokens its tiles are
-// narrower and it is the shorter everywhere (64 x 1024 -> 8192: 7.8, 5.6; 64 x 512 -> 640: 4.9, 4.9).
+// The split kernel's, 128 tokens wide. E.g. (pairs, split) 128 x 512 -> 640: 4.8 us, 6.2; 128 x 1024 ->
+// 8192: 6.9, 7.0; 128 x 8192 -> 1024: 17.1, 9.6; 200 x 2880 -> 5120: 10.3, 12.5; 300 x 8192 -> 1024: 17.4,
+// 11.0; 300 x 4096 -> 4096: 12.3, 15.1; 4000 x 8192 -> 256: 20.5, 16.4. Up to 64 tokens its tiles are
+// narrower and it is the shorter everywhere (64 x 1024 -> 8192: 7.5, 5.5; 64 x 512 -> 640: 4.8, 4.8).
 int64_t split_ns(const LinearFusedArgs& p, int sms) {
   using namespace linf;
   const int64_t tiles = cdiv(p.N, split::BM) * cdiv(p.T, 128);

@@ -13,8 +13,8 @@
 // across the reduction, and every output is written once.
 //
 // One CTA per row, or one warp per row for many short rows; the rule and what it measured
-// stand at launch_rmsnorm. 4096 x 2880 with a residual and a static scale (82.6 MB): 17.2 us,
-// 4.8 TB/s; 16384 x 2880 to bf16 (377 MB): 60 us, 6.3 TB/s. CTAs that walk the rows with the next
+// stand at launch_rmsnorm. 4096 x 2880 with a residual and a static scale (82.6 MB): 15.8 us,
+// 5.2 TB/s; 16384 x 2880 to bf16 (377 MB): 58.8 us, 6.4 TB/s. CTAs that walk the rows with the next
 // one's loads in flight were no faster (17.5 and 69 us).
 #include <algorithm>
 #include <cfloat>
@@ -181,9 +181,15 @@ cudaError_t launch_variant(const NormArgs& p, unsigned grid, int threads, cudaSt
 // Few rows (fewer than four for every SM): one vector a thread, the shortest chain. Many rows:
 // four 16-byte loads in flight a thread, so two vectors with a residual and four without;
 // rows of up to 512 values then take a warp each. On a B200 at 4096 x 2880 with a residual,
-// one vector against two: 18.5 / 17.2 us (static scale), 20.7 / 19.2 us (token scale); a warp
-// per row 19.1 / 20.5 us. At 9973 x 4096 without one, one / two / four vectors: 37.4 / 30.6 /
-// 28.7 us. At 16000 x 512, a warp per row 13.0 us, a CTA 14.6 us.
+// one vector against two: 17.1 / 15.8 us (static scale), 19.2 / 17.8 us (token scale). At 9973 x 4096
+// without one, one / two / four vectors: 36.9 / 29.4 / 27.5 us. At 16000 x 512 with one, a warp per
+// row 12.4 us, a CTA 17.8 us.
+//
+// Longer rows hold more a thread: two vectors up to 8192 values, four up to 16384, eight above. 4096 rows
+// with a residual, static and token scales: H = 8192 38 and 43 us (6.1 and 5.5 TB/s), 16384 73 and
+// 107, 32768 185 and 224 (5.1 and 4.2 TB/s); one row of 32768 4.8 and 7.6. Token scales keep the
+// products beside the row: at eight vectors that is past the 128 registers of 512 threads, and 352
+// bytes a thread spill.
 cudaError_t launch_rmsnorm(const NormArgs& p, int sms, cudaStream_t st) {
   const int nv = p.H / 8;
   const bool many = p.T >= 4 * sms;
