@@ -35,12 +35,13 @@
 // keys, 64 heads over 8 of 64 (154 MB): 46 us, 3.3 TB/s; 3 sequences of up to 131072 keys, 2 queries
 // each, 32 heads over 8 of 128 (318 MB): 84 us (up to 91 in long loops, where the power cap lowers the
 // clock), 3.8 TB/s; one query over a window of 128: 5.8 us (4.8 in a graph). Of the first, about 9 us
-// are launches, the start's chain of loads (lengths, table, keys) and the joining kernel. Many
-// queries a sequence read and expand every key again for each 16 rows: 128 queries of 64 heads over 8
-// of 64 take 111 us over 8192 keys and 361 over 32768 (154 and 190 TF/s). The products are paced by the integer pipe (code expansion, 64 lanes a cycle:
-// half of the cycles), the matrix instructions, which on this part take issue slots from it (an
-// m16n8k16 between such instructions costs about 5 cycles beyond its own 8), and by latency: twelve
-// warps issue in half of the cycles, and more do not fit the registers.
+// are launches, the start's chain of loads (lengths, table, keys) and the joining kernel. The products
+// are paced by the integer pipe (code expansion, 64 lanes a cycle: half of the cycles), the matrix
+// instructions, which on this part take issue slots from it (an m16n8k16 between such instructions
+// costs about 5 cycles beyond its own 8), and by latency: twelve warps issue in half of the cycles, and
+// more do not fit the registers. Many queries a sequence read and expand every key again for each 16
+// rows: 128 queries of 64 heads over 8 of 64 take 111 us over 8192 keys and 361 over 32768 (154 and
+// 190 TF/s).
 #include <algorithm>
 
 #include "common.cuh"
@@ -173,6 +174,12 @@ __device__ __forceinline__ uint32_t exponent_of(uint32_t word, int k) {
 constexpr float kUndo = 0x1p-15f;
 // 2^(e - 127) of an fp32's exponent field; the least, 2^-127, is a subnormal
 __device__ __forceinline__ float power_of(int field) { return __int_as_float(max(field, 1 << 22)); }
+
+// 2^(15 + e - E) of exponent fields, zero below the normal numbers. (A key above E gives nothing of use;
+// its place is written anew.)
+__device__ __forceinline__ float weight_factor(uint32_t e, int E) {
+  return __int_as_float(max(static_cast<int>(e - static_cast<uint32_t>(E) + (142u << 23)), 0));
+}
 
 // 2^d, which may lie outside of fp32, as two finite factors: a zero stays a zero
 struct Power2 {
@@ -621,7 +628,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k) {
           f[k] = __uint_as_float(exponent_of(sc[e], k));
-          f[S::kBlocks + k] = __int_as_float(max(static_cast<int>(exponent_of(ev[e], k)) - E[k] + (142 << 23), 0));
+          f[S::kBlocks + k] = weight_factor(exponent_of(ev[e], k), E[k]);
         }
 #pragma unroll
         for (int k = 0; k < 2 * S::kBlocks; k += 4)
@@ -792,7 +799,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv_attention_kernel
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k)
             factors[(32 * e + lane) * 2 * S::kBlocks + S::kBlocks + k] =
-                (out >> e) & 1 ? 0.f : __int_as_float(max(static_cast<int>(exponent_of(v[e], k)) - E[k] + (142 << 23), 0));
+                (out >> e) & 1 ? 0.f : weight_factor(exponent_of(v[e], k), E[k]);
         }
         __syncwarp();
 #pragma unroll
