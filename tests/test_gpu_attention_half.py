@@ -220,3 +220,53 @@ def test_the_norm_and_the_expert_layer_against_the_oracle(B, T, E, H, I):
         fill(n)
         graph.replay()
         check(got)
+
+
+def test_two_threads_on_two_streams(B):
+    """Calls from two host threads at once, each on its own stream with its own buffers: the results are
+    those of one thread alone."""
+    import threading
+    g = torch.Generator(device="cuda").manual_seed(8)
+    L = Layer(seed=2)
+    n = 5
+
+    def make():
+        cache = [torch.full((2 * n, HKV, PAGE, d), 255, dtype=torch.uint8, device="cuda") for d in (D // 2, D // 32) * 2]
+        table = torch.randperm(2 * n, generator=g, device="cuda").view(n, 2).int()
+        lens = torch.tensor([1, 16, 17, 30, 32], dtype=torch.int32, device="cuda")
+        fill = torch.randn(2 * n * PAGE, 2 * HKV, D, generator=g, device="cuda").bfloat16()
+        B.mxfp4_kv_append(fill[:, :HKV], fill[:, HKV:], torch.arange(2 * n * PAGE, device="cuda"), *cache)
+        last = lens.long() - 1
+        slots = table[torch.arange(n, device="cuda"), last // PAGE].long() * PAGE + last % PAGE
+        x, res = (torch.randn(n, H, generator=g, device="cuda").bfloat16() for _ in range(2))
+        return x, res, cache, table, lens, slots
+
+    def run(s, out, times):
+        for _ in range(times):
+            x, res, *rest = s
+            out.append(L.run(B, x, res.clone(), *rest, 1))
+
+    states, want = [make(), make()], [[], []]
+    for s, w in zip(states, want):
+        run(s, w, 1)
+    B.mxmoe_check()
+    got, streams, errors = [[], []], [torch.cuda.Stream(), torch.cuda.Stream()], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                run(states[i], got[i], 60)
+                streams[i].synchronize()
+        except Exception as e:      # a thread's failure is the test's
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not errors and not any(t.is_alive() for t in threads)
+    for i in range(2):
+        assert len(got[i]) == 60 and all(torch.equal(a, b) for o in got[i] for a, b in zip(o, want[i][0]))
+    B.mxmoe_check()

@@ -130,3 +130,30 @@ def test_longest_sequences(B, n, Lq, G):
                                 window=window)
     B.mxmoe_check()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_calls_with_outliers(B, seed):
+    """Shapes, windows and lengths at random, some keys' values 2^-20 to 2^50 of the rest, most of them where
+    the queries of a call begin or end to differ in what they see."""
+    import random
+    r = random.Random(seed)
+    D, Hkv, G, Lq = r.choice((64, 128)), r.choice((1, 2, 3)), r.choice((1, 2, 3, 4, 5, 6, 7, 8, 12, 20)), r.choice((1, 2, 2, 3, 5, 17))
+    page, window = r.choice((16, 32, 64, 128, 256)), r.choice((0, 0, 1, 5, 37, 64, 100, 700))
+    n = r.choice((1, 2, 5, 40, 130))
+    top = r.choice((3, 40, 130, 700, 3000)) // (4 if n > 5 else 1) + 1
+    lens = [r.choice((0, 1, Lq, Lq + 1, top, r.randint(0, top))) for _ in range(n)]
+    c = Case(B, lens, Lq, Hkv * G, Hkv, D, page, window=window, sinks=r.random() < 0.5, seed=seed, vspread=float(r.choice((0, 1, 3))))
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for b in range(min(n, 8)):
+        for _ in range(r.choice((0, 1, 2, 4)) if lens[b] else 0):
+            at = r.choice((lens[b] - 1, lens[b] - 2, lens[b] - Lq - window, lens[b] - Lq - window + 1, r.randint(0, lens[b] - 1)))
+            v = torch.randn(1, Hkv, D // 32, 32, generator=g, device="cuda")
+            v[:, :, r.randrange(D // 32):] *= 2.0 ** r.choice((-20, 5, 6, 20, 50))
+            k = torch.randn(1, Hkv, D, generator=g, device="cuda").bfloat16()
+            place = torch.tensor([min(max(at, 0), lens[b] - 1)], device="cuda")
+            B.mxfp4_kv_append(k, v.flatten(2).bfloat16(), _slots(c, b, place), *c.cache)
+    out = c.run(B)
+    B.mxmoe_check()
+    check(c, out, {(b, i) for b in range(min(n, 10)) for i in range(Lq)})
+    assert torch.equal(c.run(B), out)
